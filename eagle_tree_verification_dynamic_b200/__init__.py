@@ -43,6 +43,7 @@ from ._lib import (  # noqa: F401
     lib,
     pool_size,
     row_stats,
+    shared_attention_workspace_bytes,
     static_template_from_paths,
     static_tree_build,
     static_tree_rows,
@@ -53,6 +54,10 @@ from ._lib import (  # noqa: F401
     tree_attention_into,
     tree_attention_paged,
     tree_attention_paged_into,
+    tree_attention_shared,
+    tree_attention_shared_into,
+    tree_attention_shared_paged,
+    tree_attention_shared_paged_into,
     tree_build,
     tree_build_into,
     tree_build_workspace_bytes,

@@ -98,6 +98,18 @@ _SIGS = {
                                      ctypes.POINTER(ctypes.c_double)]),
     "eagle_tree_attention_paged": (_c_i, [_c_p, _c_p, _c_p, _c_i, _c_i, _c_p, _c_i, _c_p, _c_p, _c_p, _c_p, _c_p,
                                           _c_i, _c_i, _c_i, _c_i, _c_i, _c_i, _c_f, _c_p, _c_p, _c_sz, _c_p]),
+    "eagle_tree_attention_sinks_workspace_bytes": (_c_sz, [_c_i, _c_i, _c_i, _c_i, _c_i, _c_i, _c_i, _c_i]),
+    "eagle_tree_attention_with_sinks": (_c_i, [_c_p, _c_p, _c_p, _c_p, _c_i, _c_p, _c_p, _c_p, _c_p, _c_i, _c_i, _c_i,
+                                               _c_i, _c_i, _c_i, _c_i, _c_f, _c_p, _c_p, _c_sz, _c_p]),
+    "eagle_tree_attention_paged_with_sinks": (_c_i, [_c_p, _c_p, _c_p, _c_i, _c_i, _c_p, _c_i, _c_p, _c_p, _c_p, _c_p,
+                                                     _c_p, _c_i, _c_i, _c_i, _c_i, _c_i, _c_i, _c_i, _c_f, _c_p, _c_p,
+                                                     _c_sz, _c_p]),
+    "eagle_tree_attention_shared_workspace_bytes": (_c_sz, [_c_i, _c_i, _c_i, _c_i, _c_i, _c_i, _c_i]),
+    "eagle_tree_attention_shared": (_c_i, [_c_p, _c_p, _c_p, _c_i, _c_p, _c_p, _c_p, _c_p, _c_i, _c_p, _c_p, _c_p,
+                                           _c_i, _c_i, _c_i, _c_i, _c_i, _c_f, _c_p, _c_p, _c_sz, _c_p]),
+    "eagle_tree_attention_shared_paged": (_c_i, [_c_p, _c_p, _c_p, _c_i, _c_i, _c_p, _c_i, _c_p, _c_p, _c_i, _c_p,
+                                                 _c_p, _c_p, _c_p, _c_i, _c_i, _c_i, _c_i, _c_i, _c_f, _c_p, _c_p,
+                                                 _c_sz, _c_p]),
     "eagle_kv_compact_paged": (_c_i, [_c_p, _c_p, _c_p, _c_p, _c_p, _c_p, _c_p, _c_i, _c_i, _c_p, _c_i, _c_p, _c_i,
                                       _c_i, _c_i, _c_i, _c_i, _c_p]),
     "eagle_kv_compact": (_c_i, [_c_p, _c_p, _c_p, _c_p, _c_p, _c_p, _c_p, _c_p, _c_i, _c_i, _c_i, _c_i, _c_i, _c_i,
@@ -155,12 +167,40 @@ def _dtype_code(t: torch.Tensor) -> int:
 
 
 def _need_cuda(*ts):
+    first = None
     for t in ts:
         if t is not None:
             if not t.is_cuda:
                 raise EagleError("tensors must be on a CUDA device")
             if not t.is_contiguous():
                 raise EagleError("tensors must be contiguous")
+            first = t if first is None else first
+            if t.device != first.device:
+                raise EagleError("tensors must be on one device")
+
+
+def _need_bf16(*ts):
+    for t in ts:
+        if t.dtype != torch.bfloat16:
+            raise EagleError("attention tensors must be bf16")
+
+
+def _attention_shapes(q, caches, tree_kv, mask, prefix_len):
+    """What the C call cannot see from pointers: the sizes of q, the tree's K/V, the caches, mask and lengths agree."""
+    if q.dim() != 4:
+        raise EagleError("q must be [B][n][Hq][D]")
+    B, n, _, D = q.shape
+    for t in tree_kv:
+        if t.dim() != 4 or t.shape != tree_kv[0].shape or t.shape[:2] != q.shape[:2] or t.shape[3] != D:
+            raise EagleError("tree keys and values must be [B][n][Hkv][D]")
+    for t in caches or ():
+        if t.dim() != 4 or t.shape != caches[0].shape or t.shape[0] != B or t.shape[3] != D or \
+                t.shape[1] != tree_kv[0].shape[2]:
+            raise EagleError("caches must be [B][Hkv][Lmax][D]")
+    if mask.shape != (B, n, 2) or mask.dtype != torch.int64:
+        raise EagleError("mask must be [B][n][2] int64")
+    if prefix_len.numel() != B or prefix_len.dtype != torch.int32:
+        raise EagleError("prefix_len must be [B] int32")
 
 
 def _workspace(nbytes: int, device) -> torch.Tensor:
@@ -274,23 +314,24 @@ def tree_mask(parents: torch.Tensor, depth: Optional[torch.Tensor] = None,
 
 
 # ----------------------------------------------------------- tree attention
-def attention_workspace_bytes(B, n, Hq, Hkv, D, Lmax, window=0) -> int:
-    return lib().eagle_tree_attention_workspace_bytes(B, n, Hq, Hkv, D, Lmax, window)
+def attention_workspace_bytes(B, n, Hq, Hkv, D, Lmax, window=0, sinks=0) -> int:
+    return lib().eagle_tree_attention_sinks_workspace_bytes(B, n, Hq, Hkv, D, Lmax, window, sinks)
 
 
 def tree_attention_into(q, k_cache, v_cache, prefix_len, k_tree, v_tree, mask, pos, out, ws,
-                        window: int = 0, scale: float = 0.0):
+                        window: int = 0, scale: float = 0.0, sinks: int = 0):
     B, n, Hq, D = q.shape
     Hkv, Lmax = k_cache.shape[1], k_cache.shape[2]
-    _check(lib().eagle_tree_attention(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(prefix_len), Lmax,
-                                      _ptr(k_tree), _ptr(v_tree), _ptr(mask), _ptr(pos), B, n, Hq, Hkv, D,
-                                      window, scale, _ptr(out), _ptr(ws), ws.numel(), _stream(q.device)),
-           "eagle_tree_attention")
+    _check(lib().eagle_tree_attention_with_sinks(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(prefix_len), Lmax,
+                                                 _ptr(k_tree), _ptr(v_tree), _ptr(mask), _ptr(pos), B, n, Hq, Hkv, D,
+                                                 window, sinks, scale, _ptr(out), _ptr(ws), ws.numel(),
+                                                 _stream(q.device)), "eagle_tree_attention")
 
 
 def tree_attention(q, k_cache, v_cache, prefix_len, k_tree, v_tree, mask, pos=None, window: int = 0,
-                   scale: float = 0.0, check: bool = True) -> torch.Tensor:
-    """q [B][n][Hq][D] bf16, caches [B][Hkv][Lmax][D] bf16, tree K/V [B][n][Hkv][D] bf16 -> out bf16."""
+                   scale: float = 0.0, check: bool = True, sinks: int = 0) -> torch.Tensor:
+    """q [B][n][Hq][D] bf16, caches [B][Hkv][Lmax][D] bf16, tree K/V [B][n][Hkv][D] bf16 -> out bf16.
+    sinks: with a window, the first `sinks` keys stay visible."""
     _need_cuda(q, k_cache, v_cache, prefix_len, k_tree, v_tree, mask, pos)
     for t in (q, k_cache, v_cache, k_tree, v_tree):
         if t.dtype != torch.bfloat16:
@@ -298,8 +339,8 @@ def tree_attention(q, k_cache, v_cache, prefix_len, k_tree, v_tree, mask, pos=No
     B, n, Hq, D = q.shape
     Hkv, Lmax = k_cache.shape[1], k_cache.shape[2]
     out = torch.empty_like(q)
-    ws = _workspace(attention_workspace_bytes(B, n, Hq, Hkv, D, Lmax, window), q.device)
-    tree_attention_into(q, k_cache, v_cache, prefix_len, k_tree, v_tree, mask, pos, out, ws, window, scale)
+    ws = _workspace(attention_workspace_bytes(B, n, Hq, Hkv, D, Lmax, window, sinks), q.device)
+    tree_attention_into(q, k_cache, v_cache, prefix_len, k_tree, v_tree, mask, pos, out, ws, window, scale, sinks)
     if check:
         check_attention_status(ws)
     return out
@@ -322,27 +363,104 @@ def check_attention_status(ws: torch.Tensor):
 
 # ------------------------------------------------------- paged prefix cache
 def tree_attention_paged_into(q, k_pages, v_pages, block_table, prefix_len, k_tree, v_tree, mask, pos, out, ws,
-                              window: int = 0, scale: float = 0.0):
+                              window: int = 0, scale: float = 0.0, sinks: int = 0):
     """k_pages / v_pages [num_pages][Hkv][page_size][D] bf16, block_table [B][pages_per_seq] int32."""
     B, n, Hq, D = q.shape
     num_pages, Hkv, ps = k_pages.shape[0], k_pages.shape[1], k_pages.shape[2]
-    _check(lib().eagle_tree_attention_paged(_ptr(q), _ptr(k_pages), _ptr(v_pages), num_pages, ps, _ptr(block_table),
-                                            block_table.shape[1], _ptr(prefix_len), _ptr(k_tree), _ptr(v_tree),
-                                            _ptr(mask), _ptr(pos), B, n, Hq, Hkv, D, window, scale, _ptr(out),
-                                            _ptr(ws), ws.numel(), _stream(q.device)), "eagle_tree_attention_paged")
+    _check(lib().eagle_tree_attention_paged_with_sinks(
+        _ptr(q), _ptr(k_pages), _ptr(v_pages), num_pages, ps, _ptr(block_table), block_table.shape[1],
+        _ptr(prefix_len), _ptr(k_tree), _ptr(v_tree), _ptr(mask), _ptr(pos), B, n, Hq, Hkv, D, window, sinks, scale,
+        _ptr(out), _ptr(ws), ws.numel(), _stream(q.device)), "eagle_tree_attention_paged")
 
 
 def tree_attention_paged(q, k_pages, v_pages, block_table, prefix_len, k_tree, v_tree, mask, pos=None,
-                         window: int = 0, scale: float = 0.0, check: bool = True) -> torch.Tensor:
+                         window: int = 0, scale: float = 0.0, check: bool = True, sinks: int = 0) -> torch.Tensor:
     """Tree attention over a paged prefix cache -> out [B][n][Hq][D] bf16 (raises on a device status when
     check, e.g. a page id outside the pool for a key in use)."""
     _need_cuda(q, k_pages, v_pages, block_table, prefix_len, k_tree, v_tree, mask, pos)
     B, n, Hq, D = q.shape
     Hkv, ps = k_pages.shape[1], k_pages.shape[2]
     out = torch.empty_like(q)
-    ws = _workspace(attention_workspace_bytes(B, n, Hq, Hkv, D, block_table.shape[1] * ps, window), q.device)
+    ws = _workspace(attention_workspace_bytes(B, n, Hq, Hkv, D, block_table.shape[1] * ps, window, sinks), q.device)
     tree_attention_paged_into(q, k_pages, v_pages, block_table, prefix_len, k_tree, v_tree, mask, pos, out, ws,
-                              window, scale)
+                              window, scale, sinks)
+    if check:
+        check_attention_status(ws)
+    return out
+
+
+# ------------------------------------------- prefix shared by the whole batch
+def shared_attention_workspace_bytes(B, n, Hq, Hkv, D, Lshared, Lmax) -> int:
+    """Paged: Lshared and Lmax are the tables' capacities, pages x page_size."""
+    return lib().eagle_tree_attention_shared_workspace_bytes(B, n, Hq, Hkv, D, Lshared, Lmax)
+
+
+def tree_attention_shared_into(q, k_shared, v_shared, shared_len, k_cache, v_cache, prefix_len, k_tree, v_tree, mask,
+                               out, ws, scale: float = 0.0):
+    B, n, Hq, D = q.shape
+    Hkv, Lmax = k_cache.shape[1], k_cache.shape[2]
+    _check(lib().eagle_tree_attention_shared(
+        _ptr(q), _ptr(k_shared), _ptr(v_shared), k_shared.shape[1], _ptr(shared_len), _ptr(k_cache), _ptr(v_cache),
+        _ptr(prefix_len), Lmax, _ptr(k_tree), _ptr(v_tree), _ptr(mask), B, n, Hq, Hkv, D, scale, _ptr(out), _ptr(ws),
+        ws.numel(), _stream(q.device)), "eagle_tree_attention_shared")
+
+
+def tree_attention_shared(q, k_shared, v_shared, shared_len, k_cache, v_cache, prefix_len, k_tree, v_tree, mask,
+                          scale: float = 0.0, check: bool = True) -> torch.Tensor:
+    """Tree attention where every sequence begins with the same shared_len [1] (int32, device) keys, k_shared /
+    v_shared [Hkv][Lshared][D] bf16, read once for the batch; caches and prefix_len hold what follows them."""
+    _need_cuda(q, k_shared, v_shared, shared_len, k_cache, v_cache, prefix_len, k_tree, v_tree, mask)
+    _attention_shapes(q, (k_cache, v_cache), (k_tree, v_tree), mask, prefix_len)
+    _need_bf16(q, k_shared, v_shared, k_cache, v_cache, k_tree, v_tree)
+    B, n, Hq, D = q.shape
+    Hkv, Lmax = k_cache.shape[1], k_cache.shape[2]
+    for t in (k_shared, v_shared):
+        if t.dim() != 3 or t.shape != k_shared.shape or t.shape[0] != Hkv or t.shape[2] != D:
+            raise EagleError("shared keys and values must be [Hkv][Lshared][D]")
+    if shared_len.numel() != 1 or shared_len.dtype != torch.int32:
+        raise EagleError("shared_len must hold one int32")
+    out = torch.empty_like(q)
+    ws = _workspace(shared_attention_workspace_bytes(B, n, Hq, Hkv, D, k_shared.shape[1], Lmax), q.device)
+    tree_attention_shared_into(q, k_shared, v_shared, shared_len, k_cache, v_cache, prefix_len, k_tree, v_tree, mask,
+                               out, ws, scale)
+    if check:
+        check_attention_status(ws)
+    return out
+
+
+def tree_attention_shared_paged_into(q, k_pages, v_pages, shared_table, shared_len, block_table, prefix_len, k_tree,
+                                     v_tree, mask, out, ws, scale: float = 0.0):
+    """shared_table [shared_pages] int32: the pages of the keys that every sequence begins with."""
+    B, n, Hq, D = q.shape
+    num_pages, Hkv, ps = k_pages.shape[0], k_pages.shape[1], k_pages.shape[2]
+    _check(lib().eagle_tree_attention_shared_paged(
+        _ptr(q), _ptr(k_pages), _ptr(v_pages), num_pages, ps, _ptr(shared_table), shared_table.shape[0],
+        _ptr(shared_len), _ptr(block_table), block_table.shape[1], _ptr(prefix_len), _ptr(k_tree), _ptr(v_tree),
+        _ptr(mask), B, n, Hq, Hkv, D, scale, _ptr(out), _ptr(ws), ws.numel(), _stream(q.device)),
+        "eagle_tree_attention_shared_paged")
+
+
+def tree_attention_shared_paged(q, k_pages, v_pages, shared_table, shared_len, block_table, prefix_len, k_tree, v_tree,
+                                mask, scale: float = 0.0, check: bool = True) -> torch.Tensor:
+    """tree_attention_shared over a paged cache: the shared keys' pages in shared_table, each sequence's own in
+    block_table (raises on a device status when check, e.g. a page id outside the pool for a key in use)."""
+    _need_cuda(q, k_pages, v_pages, shared_table, shared_len, block_table, prefix_len, k_tree, v_tree, mask)
+    _attention_shapes(q, None, (k_tree, v_tree), mask, prefix_len)
+    _need_bf16(q, k_pages, v_pages, k_tree, v_tree)
+    B, n, Hq, D = q.shape
+    Hkv, ps = k_pages.shape[1], k_pages.shape[2]
+    if k_pages.dim() != 4 or v_pages.shape != k_pages.shape or Hkv != k_tree.shape[2] or k_pages.shape[3] != D:
+        raise EagleError("page pools must be [num_pages][Hkv][page_size][D]")
+    if block_table.dim() != 2 or block_table.shape[0] != B or shared_table.dim() != 1 or \
+            block_table.dtype != torch.int32 or shared_table.dtype != torch.int32:
+        raise EagleError("tables must be int32, block_table [B][pages_per_seq] and shared_table [shared_pages]")
+    if shared_len.numel() != 1 or shared_len.dtype != torch.int32:
+        raise EagleError("shared_len must hold one int32")
+    out = torch.empty_like(q)
+    ws = _workspace(shared_attention_workspace_bytes(B, n, Hq, Hkv, D, shared_table.shape[0] * ps,
+                                                     block_table.shape[1] * ps), q.device)
+    tree_attention_shared_paged_into(q, k_pages, v_pages, shared_table, shared_len, block_table, prefix_len, k_tree,
+                                     v_tree, mask, out, ws, scale)
     if check:
         check_attention_status(ws)
     return out

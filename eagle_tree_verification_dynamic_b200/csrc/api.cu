@@ -157,31 +157,19 @@ eagle_status eagle_tree_mask(const int32_t* parents, const int32_t* depth, const
 
 // ------------------------------------------------------------- tree attention
 size_t eagle_tree_attention_workspace_bytes(int B, int n, int Hq, int Hkv, int D, int Lmax, int window) {
-  if (B <= 0 || n <= 0 || Hq <= 0 || Hkv <= 0 || D <= 0 || Lmax < 0) return 0;
-  return attention_ws_bytes(B, n, Hq, Hkv, D, Lmax, window);
+  return eagle_tree_attention_sinks_workspace_bytes(B, n, Hq, Hkv, D, Lmax, window, 0);
 }
 
-eagle_status eagle_tree_attention(const void* q, const void* k_cache, const void* v_cache,
-                                  const int32_t* prefix_len, int Lmax, const void* k_tree, const void* v_tree,
-                                  const uint64_t* mask, const int32_t* pos, int B, int n, int Hq, int Hkv, int D,
-                                  int window, float scale, void* out, void* workspace, size_t workspace_bytes,
-                                  void* stream) {
-  if (!q || !k_tree || !v_tree || !mask || !prefix_len || !out) return EAGLE_ERR_NULL;
-  if (Lmax > 0 && (!k_cache || !v_cache)) return EAGLE_ERR_NULL;
-  if (window > 0 && !pos) return EAGLE_ERR_NULL;
-  if (B <= 0 || n <= 0 || Hq <= 0 || Hkv <= 0 || Lmax < 0 || window < 0) return EAGLE_ERR_SHAPE;
-  if (Hq % Hkv != 0) return EAGLE_ERR_SHAPE;
-  if (D != 64 && D != 128) return EAGLE_ERR_LIMIT;
-  if (n > EAGLE_MAX_NODES) return EAGLE_ERR_LIMIT;
-  if (!aligned16(q) || !aligned16(k_tree) || !aligned16(v_tree) || !aligned16(out) ||
-      (Lmax > 0 && (!aligned16(k_cache) || !aligned16(v_cache))))
-    return EAGLE_ERR_ALIGN;
-  eagle_status st = check_ws(workspace, workspace_bytes, attention_ws_bytes(B, n, Hq, Hkv, D, Lmax, window));
-  if (st != EAGLE_OK) return st;
-  if (!(scale > 0.f)) scale = 1.0f / sqrtf((float)D);
-  return cuda_status(launch_tree_attention(q, k_cache, v_cache, prefix_len, Lmax, k_tree, v_tree, mask, pos, B, n,
-                                           Hq, Hkv, D, window, scale, out, workspace,
-                                           static_cast<cudaStream_t>(stream)));
+size_t eagle_tree_attention_sinks_workspace_bytes(int B, int n, int Hq, int Hkv, int D, int Lmax, int window,
+                                                  int sinks) {
+  if (B <= 0 || n <= 0 || Hq <= 0 || Hkv <= 0 || D <= 0 || Lmax < 0 || sinks < 0) return 0;
+  return attention_ws_bytes({B, n, Hq, Hkv, D, Lmax, window, sinks, 0});
+}
+
+size_t eagle_tree_attention_shared_workspace_bytes(int B, int n, int Hq, int Hkv, int D, int Lshared, int Lmax) {
+  if (B <= 0 || n <= 0 || Hq <= 0 || Hkv <= 0 || D <= 0 || Lshared < 0 || Lmax < 0) return 0;
+  if ((long long)B * n * (Hq / Hkv) > 0x7fffffffLL - kAttnRowsPerUnit) return 0;
+  return attention_ws_bytes({B, n, Hq, Hkv, D, Lmax, 0, 0, Lshared});
 }
 
 }  // extern "C"
@@ -199,9 +187,62 @@ eagle_status check_paged(const int32_t* block_table, int page_size, int pages_pe
   return EAGLE_OK;
 }
 
+// The checks that every tree attention shares, then the launch.
+eagle_status attention(AttnCall k, size_t workspace_bytes, void* stream) {
+  const bool paged = k.pg != nullptr, shared = k.shared_len != nullptr;
+  if (!k.q || !k.kt || !k.vt || !k.mask || !k.plen || !k.out) return EAGLE_ERR_NULL;
+  if ((paged || k.Lmax > 0) && (!k.kc || !k.vc)) return EAGLE_ERR_NULL;
+  if (shared && (paged ? k.shared_pages > 0 && !k.shared_table : k.Lshared > 0 && (!k.ks || !k.vs)))
+    return EAGLE_ERR_NULL;
+  if (k.window > 0 && !k.pos) return EAGLE_ERR_NULL;
+  if (paged) {
+    const eagle_status st = check_paged(k.pg->block_table, k.pg->page_size, k.pg->pages_per_seq, k.pg->num_pages, k.Hkv);
+    if (st != EAGLE_OK) return st;
+    if (k.shared_pages < 0) return EAGLE_ERR_SHAPE;
+    if ((long long)k.shared_pages * k.pg->page_size > (1LL << 30)) return EAGLE_ERR_LIMIT;
+    k.Lmax = k.pg->pages_per_seq * k.pg->page_size;
+    if (shared) k.Lshared = k.shared_pages * k.pg->page_size;
+  }
+  if (k.B <= 0 || k.n <= 0 || k.Hq <= 0 || k.Hkv <= 0 || k.Lmax < 0 || k.window < 0 || k.sinks < 0 || k.Lshared < 0)
+    return EAGLE_ERR_SHAPE;
+  if (k.Hq % k.Hkv != 0) return EAGLE_ERR_SHAPE;
+  if (k.D != 64 && k.D != 128) return EAGLE_ERR_LIMIT;
+  if (k.n > EAGLE_MAX_NODES) return EAGLE_ERR_LIMIT;
+  if (shared && (long long)k.B * k.n * (k.Hq / k.Hkv) > 0x7fffffffLL - kAttnRowsPerUnit) return EAGLE_ERR_LIMIT;
+  if (!aligned16(k.q) || !aligned16(k.kt) || !aligned16(k.vt) || !aligned16(k.out) ||
+      (k.Lmax > 0 && (!aligned16(k.kc) || !aligned16(k.vc))) ||
+      (shared && !paged && k.Lshared > 0 && (!aligned16(k.ks) || !aligned16(k.vs))))
+    return EAGLE_ERR_ALIGN;
+  const eagle_status st = check_ws(k.ws, workspace_bytes,
+                                   attention_ws_bytes({k.B, k.n, k.Hq, k.Hkv, k.D, k.Lmax, k.window, k.sinks, k.Lshared}));
+  if (st != EAGLE_OK) return st;
+  if (!(k.scale > 0.f)) k.scale = 1.0f / sqrtf((float)k.D);
+  return cuda_status(launch_tree_attention(k, static_cast<cudaStream_t>(stream)));
+}
+
 }  // namespace
 
 extern "C" {
+
+eagle_status eagle_tree_attention(const void* q, const void* k_cache, const void* v_cache,
+                                  const int32_t* prefix_len, int Lmax, const void* k_tree, const void* v_tree,
+                                  const uint64_t* mask, const int32_t* pos, int B, int n, int Hq, int Hkv, int D,
+                                  int window, float scale, void* out, void* workspace, size_t workspace_bytes,
+                                  void* stream) {
+  return eagle_tree_attention_with_sinks(q, k_cache, v_cache, prefix_len, Lmax, k_tree, v_tree, mask, pos, B, n, Hq, Hkv,
+                                         D, window, 0, scale, out, workspace, workspace_bytes, stream);
+}
+
+eagle_status eagle_tree_attention_with_sinks(const void* q, const void* k_cache, const void* v_cache,
+                                             const int32_t* prefix_len, int Lmax, const void* k_tree,
+                                             const void* v_tree, const uint64_t* mask, const int32_t* pos, int B,
+                                             int n, int Hq, int Hkv, int D, int window, int sinks, float scale,
+                                             void* out, void* workspace, size_t workspace_bytes, void* stream) {
+  AttnCall k = {q, k_cache, v_cache, prefix_len, Lmax, k_tree, v_tree, mask, pos, B, n, Hq, Hkv, D, window, scale, out,
+                workspace};
+  k.sinks = sinks;
+  return attention(k, workspace_bytes, stream);
+}
 
 eagle_status eagle_tree_attention_paged(const void* q, const void* k_pages, const void* v_pages, int num_pages,
                                         int page_size, const int32_t* block_table, int pages_per_seq,
@@ -209,24 +250,57 @@ eagle_status eagle_tree_attention_paged(const void* q, const void* k_pages, cons
                                         const uint64_t* mask, const int32_t* pos, int B, int n, int Hq, int Hkv,
                                         int D, int window, float scale, void* out, void* workspace,
                                         size_t workspace_bytes, void* stream) {
-  if (!q || !k_pages || !v_pages || !k_tree || !v_tree || !mask || !prefix_len || !out) return EAGLE_ERR_NULL;
-  if (window > 0 && !pos) return EAGLE_ERR_NULL;
-  eagle_status st = check_paged(block_table, page_size, pages_per_seq, num_pages, Hkv);
-  if (st != EAGLE_OK) return st;
-  if (B <= 0 || n <= 0 || Hq <= 0 || window < 0 || Hq % Hkv != 0) return EAGLE_ERR_SHAPE;
-  if (D != 64 && D != 128) return EAGLE_ERR_LIMIT;
-  if (n > EAGLE_MAX_NODES) return EAGLE_ERR_LIMIT;
-  if (!aligned16(q) || !aligned16(k_tree) || !aligned16(v_tree) || !aligned16(out) || !aligned16(k_pages) ||
-      !aligned16(v_pages))
-    return EAGLE_ERR_ALIGN;
-  const int cap = pages_per_seq * page_size;
-  st = check_ws(workspace, workspace_bytes, attention_ws_bytes(B, n, Hq, Hkv, D, cap, window));
-  if (st != EAGLE_OK) return st;
-  if (!(scale > 0.f)) scale = 1.0f / sqrtf((float)D);
+  return eagle_tree_attention_paged_with_sinks(q, k_pages, v_pages, num_pages, page_size, block_table, pages_per_seq,
+                                               prefix_len, k_tree, v_tree, mask, pos, B, n, Hq, Hkv, D, window, 0,
+                                               scale, out, workspace, workspace_bytes, stream);
+}
+
+eagle_status eagle_tree_attention_paged_with_sinks(const void* q, const void* k_pages, const void* v_pages,
+                                                   int num_pages, int page_size, const int32_t* block_table,
+                                                   int pages_per_seq, const int32_t* prefix_len, const void* k_tree,
+                                                   const void* v_tree, const uint64_t* mask, const int32_t* pos,
+                                                   int B, int n, int Hq, int Hkv, int D, int window, int sinks,
+                                                   float scale, void* out, void* workspace, size_t workspace_bytes,
+                                                   void* stream) {
   const PagedKV pg = {block_table, page_size, pages_per_seq, num_pages};
-  return cuda_status(launch_tree_attention(q, k_pages, v_pages, prefix_len, cap, k_tree, v_tree, mask, pos, B, n,
-                                           Hq, Hkv, D, window, scale, out, workspace,
-                                           static_cast<cudaStream_t>(stream), &pg));
+  AttnCall k = {q, k_pages, v_pages, prefix_len, 0, k_tree, v_tree, mask, pos, B, n, Hq, Hkv, D, window, scale, out,
+                workspace};
+  k.pg = &pg;
+  k.sinks = sinks;
+  return attention(k, workspace_bytes, stream);
+}
+
+eagle_status eagle_tree_attention_shared(const void* q, const void* k_shared, const void* v_shared, int Lshared,
+                                         const int32_t* shared_len, const void* k_cache, const void* v_cache,
+                                         const int32_t* prefix_len, int Lmax, const void* k_tree, const void* v_tree,
+                                         const uint64_t* mask, int B, int n, int Hq, int Hkv, int D, float scale,
+                                         void* out, void* workspace, size_t workspace_bytes, void* stream) {
+  if (!shared_len) return EAGLE_ERR_NULL;
+  AttnCall k = {q, k_cache, v_cache, prefix_len, Lmax, k_tree, v_tree, mask, nullptr, B, n, Hq, Hkv, D, 0, scale, out,
+                workspace};
+  k.shared_len = shared_len;
+  k.ks = k_shared;
+  k.vs = v_shared;
+  k.Lshared = Lshared;
+  return attention(k, workspace_bytes, stream);
+}
+
+eagle_status eagle_tree_attention_shared_paged(const void* q, const void* k_pages, const void* v_pages, int num_pages,
+                                               int page_size, const int32_t* shared_table, int shared_pages,
+                                               const int32_t* shared_len, const int32_t* block_table,
+                                               int pages_per_seq, const int32_t* prefix_len, const void* k_tree,
+                                               const void* v_tree, const uint64_t* mask, int B, int n, int Hq,
+                                               int Hkv, int D, float scale, void* out, void* workspace,
+                                               size_t workspace_bytes, void* stream) {
+  if (!shared_len) return EAGLE_ERR_NULL;
+  const PagedKV pg = {block_table, page_size, pages_per_seq, num_pages};
+  AttnCall k = {q, k_pages, v_pages, prefix_len, 0, k_tree, v_tree, mask, nullptr, B, n, Hq, Hkv, D, 0, scale, out,
+                workspace};
+  k.pg = &pg;
+  k.shared_len = shared_len;
+  k.shared_table = shared_table;
+  k.shared_pages = shared_pages;
+  return attention(k, workspace_bytes, stream);
 }
 
 eagle_status eagle_kv_compact_paged(const void* k_tree, const void* v_tree, const int32_t* path,
@@ -320,7 +394,7 @@ struct StepLayout {
 };
 
 // Shapes of the step; false for sizes that no call accepts (the step reports which).
-bool step_layout(const eagle_step_in_t* in, StepLayout* L) {
+bool step_layout(const eagle_step_in_t* in, int sinks, StepLayout* L) {
   if (!in || in->B <= 0 || in->V <= 0 || in->depth <= 0 || in->k <= 0 || in->m <= 0 || !valid_dtype(in->logits_dtype))
     return false;
   if (in->depth > EAGLE_MAX_DEPTH || in->k > EAGLE_MAX_TOPK || in->m > EAGLE_MAX_NODES) return false;
@@ -337,7 +411,7 @@ bool step_layout(const eagle_step_in_t* in, StepLayout* L) {
   const int eb = dtype_bytes(in->logits_dtype);
   L->build_off = 0;
   L->attn_off = align_up(tree_build_ws_bytes(in->B, L->R, in->V, eb, in->k), 256);
-  L->acc_off = align_up(L->attn_off + attention_ws_bytes(in->B, L->n, in->Hq, in->Hkv, in->D, cap, in->window), 256);
+  L->acc_off = align_up(L->attn_off + attention_ws_bytes({in->B, L->n, in->Hq, in->Hkv, in->D, cap, in->window, sinks, 0}), 256);
   L->total = align_up(L->acc_off + accept_ws_bytes(in->B, L->n, in->V, in->logits_dtype), 256);
   return true;
 }
@@ -348,12 +422,12 @@ extern "C" {
 
 size_t eagle_verify_step_workspace_bytes(const eagle_step_in_t* in) {
   StepLayout L;
-  return step_layout(in, &L) ? L.total : 0;
+  return step_layout(in, 0, &L) ? L.total : 0;
 }
 
 size_t eagle_verify_step_attention_status_offset(const eagle_step_in_t* in) {
   StepLayout L;
-  return step_layout(in, &L) ? L.attn_off : 0;
+  return step_layout(in, 0, &L) ? L.attn_off : 0;
 }
 
 eagle_status eagle_verify_step(const eagle_step_in_t* in, const eagle_step_out_t* out, int* n_nodes,
@@ -379,7 +453,7 @@ eagle_status eagle_verify_step(const eagle_step_in_t* in, const eagle_step_out_t
     return EAGLE_ERR_LIMIT;
   if (in->D != 64 && in->D != 128) return EAGLE_ERR_LIMIT;
   StepLayout L;
-  if (!step_layout(in, &L)) return EAGLE_ERR_LIMIT;
+  if (!step_layout(in, 0, &L)) return EAGLE_ERR_LIMIT;
   if ((long long)in->B * (L.n + 1) > 0x7fffffffLL) return EAGLE_ERR_SHAPE;
   if (in->uniforms && in->V > accept_max_vocab(in->logits_dtype)) return EAGLE_ERR_LIMIT;
   if (in->sampling_rule != EAGLE_SAMPLE_WITH_REPLACEMENT && in->sampling_rule != EAGLE_SAMPLE_WITHOUT_REPLACEMENT)
@@ -412,9 +486,11 @@ eagle_status eagle_verify_step(const eagle_step_in_t* in, const eagle_step_out_t
   // --- tree attention
   const float scale = in->scale > 0.f ? in->scale : 1.0f / sqrtf((float)in->D);
   const PagedKV pg = {in->block_table, in->page_size, in->pages_per_seq, in->num_pages};
-  e = launch_tree_attention(in->q, in->k_cache, in->v_cache, in->prefix_len, in->Lmax, in->k_tree, in->v_tree,
-                            out->mask, out->pos, in->B, n, in->Hq, in->Hkv, in->D, in->window, scale, out->attn_out,
-                            ws + L.attn_off, s, paged ? &pg : nullptr, /*early=*/true);
+  AttnCall at = {in->q, in->k_cache, in->v_cache, in->prefix_len, in->Lmax, in->k_tree, in->v_tree, out->mask, out->pos,
+                 in->B, n, in->Hq, in->Hkv, in->D, in->window, scale, out->attn_out, ws + L.attn_off};
+  at.pg = paged ? &pg : nullptr;
+  at.early = true;
+  e = launch_tree_attention(at, s);
   if (e != cudaSuccess) return cuda_status(e);
   // --- acceptance (the draft rows' log-sum-exps are the tree's row_lse)
   e = launch_accept(in->target_logits, in->logits_dtype, in->draft_logits, in->logits_dtype, t.row_lse, L.R,

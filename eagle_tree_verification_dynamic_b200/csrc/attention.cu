@@ -19,24 +19,35 @@ int attention_row_groups(int n, int Hq, int Hkv) {
   return (rows + kAttnRowsPerUnit - 1) / kAttnRowsPerUnit;
 }
 
-int attention_ctas(int B, int n, int Hq, int Hkv, int Lmax, int window) {
-  const long long span = window > 0 ? (Lmax < window ? Lmax : window) : Lmax;
-  const long long tiles_max = (span + kAttnKeysPerTile - 1) / kAttnKeysPerTile + (n + kAttnKeysPerTile - 1) / kAttnKeysPerTile;
-  const long long T_max = (long long)B * Hkv * attention_row_groups(n, Hq, Hkv) * tiles_max;
+int attention_shared_row_groups(const AttnShape& a) {
+  return a.Lshared > 0 ? attention_row_groups(a.B * a.n, a.Hq, a.Hkv) : 0;
+}
+
+int attention_ctas(const AttnShape& a) {
+  long long span = a.Lmax;
+  if (a.window > 0) {  // the window's keys and the sinks before them
+    const long long seen = (long long)a.window + a.sinks;
+    if (seen < span) span = seen;
+  }
+  const auto tiles = [](long long keys) { return (keys + kAttnKeysPerTile - 1) / kAttnKeysPerTile; };
+  const long long T_max =
+      (long long)a.B * a.Hkv * attention_row_groups(a.n, a.Hq, a.Hkv) * (tiles(span) + tiles(a.n)) +
+      (long long)a.Hkv * attention_shared_row_groups(a) * tiles(a.Lshared);
   const int sms = device_sm_count();
   return (int)(T_max < sms ? T_max : sms);
 }
 
-AttnWorkspace attention_ws_layout(int B, int n, int Hq, int Hkv, int D, int Lmax, int window) {
+AttnWorkspace attention_ws_layout(const AttnShape& a) {
   AttnWorkspace w;
-  const int C = attention_ctas(B, n, Hq, Hkv, Lmax, window);
-  const size_t U = (size_t)B * Hkv * attention_row_groups(n, Hq, Hkv);
+  const int C = attention_ctas(a);
+  const size_t U = (size_t)a.B * a.Hkv * attention_row_groups(a.n, a.Hq, a.Hkv) +
+                   (size_t)a.Hkv * attention_shared_row_groups(a);
   const size_t slots = (size_t)C + U;
   w.status_off = 0;
   w.cta_status_off = 256;
   w.part_lse_off = align_up(w.cta_status_off + sizeof(int) * (size_t)C, 256);
   w.part_o_off = align_up(w.part_lse_off + sizeof(float) * slots * kAttnRowsPerUnit, 256);
-  w.bytes = align_up(w.part_o_off + sizeof(float) * slots * kAttnRowsPerUnit * (size_t)D, 256);
+  w.bytes = align_up(w.part_o_off + sizeof(float) * slots * kAttnRowsPerUnit * (size_t)a.D, 256);
   return w;
 }
 

@@ -111,45 +111,104 @@ struct TcBars {
 static_assert(sizeof(TcBars) <= 512, "barrier block");  // kXchOff
 
 // ----------------------------------------------------------- tile schedule
+// The visible prefix keys of a unit come in one of three forms:
+//   kModePlain   one range: the whole prefix, or the window's part of it
+//   kModeSinks   a window and the first `sinks` keys: two ranges (one, when
+//                they meet), each cut into tiles of 64 from its own start
+//   kModeShared  the prefix is `shared` keys that every sequence of the batch
+//                has in common, then the sequence's own: the shared keys get
+//                units of their own, whose 128 rows are (node, head) pairs of
+//                the whole batch, so they are read once per 128 rows of the
+//                batch instead of once per sequence.  Every unit leaves
+//                partials there and the combine joins a row's two units.
+// In kModeShared "sequence" 0 of the schedule is the shared range and 1..B the
+// batch; in the other modes sequence b of the schedule is sequence b.
+enum AttnMode { kModePlain = 0, kModeSinks = 1, kModeShared = 2 };
+
 struct AttnGeom {
   const int32_t* plen;
   int B, Hkv, RG, n, Lmax, window, C;
   int lo_align;  // the first prefix tile starts at a multiple of this (64 for a paged cache, else 1)
+  int sinks;                   // kModeSinks
+  const int32_t* shared_len;   // kModeShared: device int, clamped to [0, Lshared]
+  int Lshared;
+  int RGs;                     // kModeShared: row groups of the whole batch's rows
 };
 
-__device__ __forceinline__ int geom_len(const AttnGeom& a, int b) {
-  return min(max(__ldg(a.plen + b), 0), a.Lmax);
+// sequences of the schedule; their row groups, nodes and first node
+template <int MODE>
+__device__ __forceinline__ int geom_seqs(const AttnGeom& a) { return MODE == kModeShared ? a.B + 1 : a.B; }
+template <int MODE>
+__device__ __forceinline__ int geom_rg(const AttnGeom& a, int b) { return MODE == kModeShared && b == 0 ? a.RGs : a.RG; }
+template <int MODE>
+__device__ __forceinline__ int geom_nodes(const AttnGeom& a, int b) {
+  return MODE == kModeShared && b == 0 ? a.B * a.n : a.n;
 }
-// first visible prefix key of a sequence of length L (the window of the
-// shallowest tree node, depth 1, at position L)
-__device__ __forceinline__ int geom_lo(const AttnGeom& a, int L) {
-  const int lo = a.window > 0 ? max(0, L - a.window + 1) : 0;
-  return lo - lo % a.lo_align;  // keys below the window start are masked row by row
+template <int MODE>
+__device__ __forceinline__ int geom_node0(const AttnGeom& a, int b) {
+  return MODE == kModeShared ? (b == 0 ? 0 : (b - 1) * a.n) : b * a.n;
 }
-__device__ __forceinline__ int geom_ptiles(const AttnGeom& a, int L) { return (L - geom_lo(a, L) + kBN - 1) / kBN; }
-__device__ __forceinline__ int geom_tiles(const AttnGeom& a, int b) {
-  return geom_ptiles(a, geom_len(a, b)) + (a.n + kBN - 1) / kBN;
+// index of unit (b, hr) among all units
+template <int MODE>
+__device__ __forceinline__ int geom_unit(const AttnGeom& a, int b, int hr) {
+  if (MODE == kModeShared) return b == 0 ? hr : a.Hkv * a.RGs + (b - 1) * a.Hkv * a.RG + hr;
+  return b * a.Hkv * a.RG + hr;
 }
 
-// Whole warp: total tiles of all units, and the first tile of sequence b_end.
+template <int MODE>
+__device__ __forceinline__ int geom_len(const AttnGeom& a, int b) {
+  if (MODE == kModeShared) {
+    if (b == 0) return min(max(__ldg(a.shared_len), 0), a.Lshared);
+    --b;
+  }
+  return min(max(__ldg(a.plen + b), 0), a.Lmax);
+}
+// first key of the window range of a sequence of length L (the window of the
+// shallowest tree node, depth 1, at position L), and kModeSinks' sink tiles
+// before it (0 when the two ranges meet: then the window range starts at 0)
+template <int MODE>
+__device__ __forceinline__ int geom_lo(const AttnGeom& a, int L) {
+  if (MODE == kModeShared) return 0;
+  const int lo = a.window > 0 ? max(0, L - a.window + 1) : 0;
+  const int at = lo - lo % a.lo_align;  // keys below the window start are masked row by row
+  if (MODE == kModeSinks && at <= (min(a.sinks, L) + kBN - 1) / kBN * kBN) return 0;
+  return at;
+}
+template <int MODE>
+__device__ __forceinline__ int geom_sink_tiles(const AttnGeom& a, int L, int lo) {
+  return MODE == kModeSinks && lo > 0 ? (a.sinks + kBN - 1) / kBN : 0;
+}
+template <int MODE>
+__device__ __forceinline__ int geom_ptiles(const AttnGeom& a, int L) {
+  const int lo = geom_lo<MODE>(a, L);
+  return geom_sink_tiles<MODE>(a, L, lo) + (L - lo + kBN - 1) / kBN;
+}
+template <int MODE>
+__device__ __forceinline__ int geom_tiles(const AttnGeom& a, int b) {
+  const int pt = geom_ptiles<MODE>(a, geom_len<MODE>(a, b));
+  return MODE == kModeShared && b == 0 ? pt : pt + (a.n + kBN - 1) / kBN;
+}
+
+// Whole warp: total tiles of all units of the schedule's sequences below b_end.
+template <int MODE>
 __device__ __forceinline__ long long geom_prefix(const AttnGeom& a, int b_end, int lane) {
-  const int HR = a.Hkv * a.RG;
   long long acc = 0;
-  for (int b = lane; b < b_end; b += 32) acc += (long long)HR * geom_tiles(a, b);
+  for (int b = lane; b < b_end; b += 32) acc += (long long)(a.Hkv * geom_rg<MODE>(a, b)) * geom_tiles<MODE>(a, b);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) acc += __shfl_xor_sync(kFull, acc, o);
   return acc;
 }
 
 // Whole warp: the unit (b, hr) holding global tile t and t's offset in it.
+template <int MODE>
 __device__ __forceinline__ void geom_locate(const AttnGeom& a, long long t, int lane, int& b_out, int& hr_out,
                                             int& off_out) {
-  const int HR = a.Hkv * a.RG;
+  const int nb = geom_seqs<MODE>(a);
   long long base = 0;
-  for (int bc = 0; bc < a.B; bc += 32) {
+  for (int bc = 0; bc < nb; bc += 32) {
     const int b = bc + lane;
-    const int tb = b < a.B ? geom_tiles(a, b) : 0;
-    const long long v = (long long)HR * tb;
+    const int tb = b < nb ? geom_tiles<MODE>(a, b) : 0;
+    const long long v = (long long)(a.Hkv * geom_rg<MODE>(a, b)) * tb;
     long long inc = v;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -157,7 +216,7 @@ __device__ __forceinline__ void geom_locate(const AttnGeom& a, long long t, int 
       if (lane >= o) inc += y;
     }
     const long long exc = inc - v;
-    const bool hit = b < a.B && base + exc <= t && t < base + inc;
+    const bool hit = b < nb && base + exc <= t && t < base + inc;
     const unsigned m = __ballot_sync(kFull, hit);
     if (m) {
       const int src = __ffs(m) - 1;
@@ -175,7 +234,7 @@ __device__ __forceinline__ void geom_locate(const AttnGeom& a, long long t, int 
     }
     base += __shfl_sync(kFull, inc, 31);
   }
-  b_out = a.B;
+  b_out = nb;
   hr_out = 0;
   off_out = 0;
 }
@@ -191,13 +250,21 @@ __device__ __forceinline__ bool cta_nonempty(int c, long long T, int C) {
 
 // One contiguous piece of a unit inside one CTA's range.
 struct Piece {
-  int b, hr;    // unit = b * HR + hr
+  int b, hr;    // sequence of the schedule and (head, row group) of the unit
   int tb, te;   // tiles [tb, te) of the unit
   int ptiles;   // the unit's prefix tiles (tiles >= ptiles are tree tiles)
-  int L, lo;    // prefix length and first visible prefix key
-  bool whole;   // the piece is the entire unit
+  int L, lo;    // prefix length and first key of its window range
+  int st;       // kModeSinks: sink tiles before the window range
+  bool whole;   // the piece is the entire unit and its result final
 };
+// first key of prefix tile t
+template <int MODE>
+__device__ __forceinline__ int piece_key0(const Piece& pc, int t) {
+  if (MODE == kModeSinks) return t < pc.st ? t * kBN : pc.lo + (t - pc.st) * kBN;
+  return pc.lo + t * kBN;
+}
 
+template <int MODE>
 struct PieceCursor {
   int b, hr, off, left;
   __device__ __forceinline__ void init(int b0, int hr0, int off0, int n_tiles) {
@@ -209,20 +276,20 @@ struct PieceCursor {
   __device__ __forceinline__ void init(const TcBars* s) { init(s->b0, s->hr0, s->off0, s->n_tiles); }
   __device__ __forceinline__ bool next(const AttnGeom& a, Piece& pc) {
     if (left <= 0) return false;
-    const int HR = a.Hkv * a.RG;
     pc.b = b;
     pc.hr = hr;
-    pc.L = geom_len(a, b);
-    pc.lo = geom_lo(a, pc.L);
-    pc.ptiles = geom_ptiles(a, pc.L);
-    const int tiles = pc.ptiles + (a.n + kBN - 1) / kBN;
+    pc.L = geom_len<MODE>(a, b);
+    pc.lo = geom_lo<MODE>(a, pc.L);
+    pc.st = geom_sink_tiles<MODE>(a, pc.L, pc.lo);
+    pc.ptiles = geom_ptiles<MODE>(a, pc.L);
+    const int tiles = MODE == kModeShared && b == 0 ? pc.ptiles : pc.ptiles + (a.n + kBN - 1) / kBN;
     const int nt = min(tiles - off, left);
     pc.tb = off;
     pc.te = off + nt;
-    pc.whole = off == 0 && nt == tiles;
+    pc.whole = MODE != kModeShared && off == 0 && nt == tiles;
     left -= nt;
     off = 0;
-    if (++hr == HR) {
+    if (++hr == a.Hkv * geom_rg<MODE>(a, b)) {
       hr = 0;
       ++b;
     }
@@ -246,6 +313,8 @@ struct TcParams {
   // block_table [B][pages_per_seq] page ids
   const int32_t* block_table;
   int page_size, pages_per_seq, num_pages;
+  const int32_t* shared_table;  // kModeShared, paged: the shared keys' page ids [shared_pages]
+  int shared_pages;
   // > 0: every softmax warp first waits this long (ns) on a barrier nothing
   // completes, so the CTA takes its abort path (eagle_debug_attention_wait_probe)
   unsigned long long probe_ns;
@@ -278,13 +347,14 @@ struct RowCtx {
   int tpos[4];        // positions of tree keys lane, 32+lane, 64+lane, 96+lane (window and tree tiles)
 };
 
+template <int MODE>
 __device__ __forceinline__ void row_issue(RowCtx& rc, const Piece& pc, const TcParams& p, int r_local, int lane,
                                           int G) {
   const AttnGeom& a = p.geo;
-  const int r_glob = (pc.hr % a.RG) * kRowsPerCta + r_local;
-  const bool row_ok = r_glob < a.n * G;
+  const int r_glob = (pc.hr % geom_rg<MODE>(a, pc.b)) * kRowsPerCta + r_local;
+  const bool row_ok = r_glob < geom_nodes<MODE>(a, pc.b) * G;
   const int qi = row_ok ? r_glob / G : 0;
-  const size_t nb = (size_t)pc.b * a.n;
+  const size_t nb = (size_t)geom_node0<MODE>(a, pc.b);
   const bool has_tree = pc.te > pc.ptiles;
   rc.mw0 = rc.mw1 = 0;
   rc.qpos = 0;
@@ -294,7 +364,7 @@ __device__ __forceinline__ void row_issue(RowCtx& rc, const Piece& pc, const TcP
     rc.mw0 = ld_early_u64(p.mask + (nb + qi) * 2);
     rc.mw1 = ld_early_u64(p.mask + (nb + qi) * 2 + 1);
   }
-  if (a.window > 0) {
+  if (MODE != kModeShared && a.window > 0) {
     if (row_ok) rc.qpos = ld_early_s32(p.pos + nb + qi);
     if (has_tree) {
 #pragma unroll
@@ -317,8 +387,10 @@ __device__ __forceinline__ int table_entry(const int32_t* bt, int idx, int width
 // as the current ones are first used, so only a piece's first lookup waits on
 // memory.  A page id outside the pool turns into a box past the end, which
 // reads zeros; if a key inside the sequence sat there, the CTA reports it.
+// (kModeSinks only reports pages that hold a key some row sees: a page between
+// the sinks and the window may have been given back.)
 // Returns false when a wait gave up.
-template <int D>
+template <int D, int MODE>
 __device__ bool produce_paged(const TcParams& p, const AttnGeom& a, const Piece& pc, int g, uint32_t s_base,
                               TcBars* bars, volatile int* abort, const CUtensorMap* tm_k, const CUtensorMap* tm_v,
                               const CUtensorMap* tm_kt, const CUtensorMap* tm_vt, int lane, int& jg) {
@@ -327,7 +399,10 @@ __device__ bool produce_paged(const TcParams& p, const AttnGeom& a, const Piece&
   const int ps = p.page_size;
   const int sub = ps < kBN ? ps : kBN;  // keys per box
   const int nsub = kBN / sub;           // boxes per tile: 1, 2 or 4
-  const int32_t* bt = p.block_table + (size_t)pc.b * p.pages_per_seq;
+  const bool in_shared = MODE == kModeShared && pc.b == 0;
+  const int width = in_shared ? p.shared_pages : p.pages_per_seq;
+  const int seq = MODE == kModeShared ? pc.b - 1 : pc.b;
+  const int32_t* bt = in_shared ? p.shared_table : p.block_table + (size_t)seq * p.pages_per_seq;
   const int past_end = p.num_pages * a.Hkv * ps;  // first row past the pools (the host keeps it in int range)
   int c0 = -64, cur = -1, nxt = -1;               // table chunk [c0, c0 + 32): lane l holds entry c0 + l
   for (int t = pc.tb; t < pc.te; ++t) {
@@ -339,13 +414,13 @@ __device__ bool produce_paged(const TcParams& p, const AttnGeom& a, const Piece&
     const uint32_t kdst = s_base + Lay::kStageOff + st * Lay::kStageBytes;
     const uint32_t vdst = kdst + Lay::kKBytes;
     if (t < pc.ptiles) {
-      const int key0 = pc.lo + t * kBN;
+      const int key0 = piece_key0<MODE>(pc, t);
       const int e0 = key0 / ps;  // the tile's first entry; its nsub entries share e0's chunk
       const int base = e0 & ~31;
       if (base != c0) {  // warp-uniform
-        cur = base == c0 + 32 ? nxt : table_entry(bt, base + lane, p.pages_per_seq);
+        cur = base == c0 + 32 ? nxt : table_entry(bt, base + lane, width);
         c0 = base;
-        nxt = table_entry(bt, c0 + 32 + lane, p.pages_per_seq);
+        nxt = table_entry(bt, c0 + 32 + lane, width);
       }
       int row[4];
       bool bad = false;
@@ -354,7 +429,9 @@ __device__ bool produce_paged(const TcParams& p, const AttnGeom& a, const Piece&
         const int page = __shfl_sync(kFull, cur, (e0 - c0 + j) & 31);  // every lane takes part
         const int kj = key0 + j * sub;
         const bool valid = page >= 0 && page < p.num_pages;
-        if (j < nsub && !valid && kj < pc.L) bad = true;
+        bool needed = kj < pc.L;
+        if (MODE == kModeSinks) needed = needed && (kj < a.sinks || kj + sub > pc.L - a.window + 1);
+        if (j < nsub && !valid && needed) bad = true;
         row[j] = valid ? (page * a.Hkv + g) * ps + kj % ps : past_end;
       }
       if (lane == 0) {
@@ -372,7 +449,7 @@ __device__ bool produce_paged(const TcParams& p, const AttnGeom& a, const Piece&
       }
     } else if (lane == 0) {
       mbar_arrive_expect_tx(fb, Lay::kStageBytes);
-      const int z = pc.b * a.n + (t - pc.ptiles) * kBN;
+      const int z = geom_node0<MODE>(a, pc.b) + (t - pc.ptiles) * kBN;
       for (int at = 0; at < Lay::kAtoms; ++at) {
         tma_load_3d(kdst + at * Lay::kKVAtomBytes, tm_kt, at * 64, g, z, fb);
         tma_load_3d(vdst + at * Lay::kKVAtomBytes, tm_vt, at * 64, g, z, fb);
@@ -383,17 +460,23 @@ __device__ bool produce_paged(const TcParams& p, const AttnGeom& a, const Piece&
   return true;
 }
 
+// The lowest `count` of 32 bits (none below 0, all from 32 on).
+__device__ __forceinline__ uint32_t low_bits(int count) {
+  return count >= 32 ? 0xffffffffu : (count > 0 ? (1u << count) - 1u : 0u);
+}
+
 // How long a waiting softmax warp or producer lane may sleep per poll (ns):
 // the MMA warp shares a scheduler with two softmax warps, and a warp that
 // polls in a tight loop takes issue slots from it.
 constexpr uint32_t kSoftmaxSleepNs = 300u;
 constexpr uint32_t kProducerSleepNs = 500u;
 
-template <int D>
+template <int D, int MODE>
 __global__ void __launch_bounds__(kTcThreads, 1)
 attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                const __grid_constant__ CUtensorMap tm_kt, const __grid_constant__ CUtensorMap tm_vt,
-               const __grid_constant__ CUtensorMap tm_q, const TcParams p) {
+               const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_ks,
+               const __grid_constant__ CUtensorMap tm_vs, const TcParams p) {
   using Lay = TcLayout<D>;
   constexpr int S = Lay::kStages;
   extern __shared__ __align__(1024) unsigned char smem[];
@@ -412,8 +495,6 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
   TcBars* bars = reinterpret_cast<TcBars*>(smem + Lay::kBarOff);
   const uint32_t s_base = smem_u32(smem);
   const int G = p.Hq / a.Hkv;
-  const int rows = a.n * G;
-  const int HR = a.Hkv * a.RG;
   volatile int* abort = &bars->abort;
 
   if (tid == 0) {
@@ -445,6 +526,10 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
     prefetch_tmap(&tm_kt);
     prefetch_tmap(&tm_vt);
     if (p.q_by_tma) prefetch_tmap(&tm_q);
+    if (MODE == kModeShared) {
+      prefetch_tmap(&tm_ks);
+      prefetch_tmap(&tm_vs);
+    }
   }
   if (warp == 0) {
     tmem_alloc(smem_u32(&bars->tmem_base), Lay::kTmemCols);
@@ -455,17 +540,17 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
   if (!p.early) griddep_wait();
   // softmax warps: cursor and the first piece's row inputs, requested before
   // the K/V stream starts
-  PieceCursor scur;
+  PieceCursor<MODE> scur;
   Piece spc;
   RowCtx src;
   bool s_have = false;
   const int quad = warp & 3;
   const int r_local = quad * 32 + lane;  // softmax: TMEM lane = row within the unit's 128
   if (warp >= 1) {
-    const long long T = geom_prefix(a, a.B, lane);
+    const long long T = geom_prefix<MODE>(a, geom_seqs<MODE>(a), lane);
     const long long t0 = (long long)c * T / a.C, t1 = (long long)(c + 1) * T / a.C;
-    int b0 = a.B, hr0 = 0, off0 = 0;
-    if (t1 > t0) geom_locate(a, t0, lane, b0, hr0, off0);
+    int b0 = geom_seqs<MODE>(a), hr0 = 0, off0 = 0;
+    if (t1 > t0) geom_locate<MODE>(a, t0, lane, b0, hr0, off0);
     if (warp == 1 && lane == 0) {
       bars->n_tiles = (int)(t1 - t0);
       bars->b0 = b0;
@@ -478,7 +563,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
       // issued before the block barrier, so ahead of the first K/V copies,
       // and consumed only at the piece's first tile: the producer does not
       // wait for them (a load issued behind the K/V stream waits microseconds)
-      if (s_have && !p.early) row_issue(src, spc, p, r_local, lane, G);
+      if (s_have && !p.early) row_issue<MODE>(src, spc, p, r_local, lane, G);
     }
   }
   // a thread lets the next kernel start only after its own griddep_wait, so
@@ -492,14 +577,16 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
-    PieceCursor cur;
+    PieceCursor<MODE> cur;
     cur.init(bars);
     Piece pc;
     int si = 0, jg = 0;  // pieces whose Q was loaded; tiles issued
     bool ok = true;
     while (ok && cur.next(a, pc)) {
       const int qb = si & 1;
-      const int g = pc.hr / a.RG, rg = pc.hr % a.RG;
+      const int RG = geom_rg<MODE>(a, pc.b);
+      const int g = pc.hr / RG, rg = pc.hr % RG;
+      const int node0 = geom_node0<MODE>(a, pc.b), rows = geom_nodes<MODE>(a, pc.b) * G;
       // Q buffer qb was last read by the QK^T of piece si - 2
       if (si >= 2 && !__all_sync(kFull, mbar_wait(smem_u32(&bars->q_empty[qb]), ((si >> 1) - 1) & 1, abort))) {
         ok = false;
@@ -514,7 +601,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
           mbar_arrive_expect_tx(qbar, Lay::kQBytes);
           const int rows_i = kRowsPerCta / G;
           for (int at = 0; at < Lay::kAtoms; ++at)
-            tma_load_3d(qdst + at * 16384, &tm_q, at * 64, g * G, pc.b * a.n + rg * rows_i, qbar);
+            tma_load_3d(qdst + at * 16384, &tm_q, at * 64, g * G, node0 + rg * rows_i, qbar);
         }
       } else {
         // gather: 16-byte pieces of the 128 rows into the swizzled K-major tile
@@ -531,7 +618,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
               const int rr = rg * kRowsPerCta + r;
               if (rr < rows) {
                 const int i = rr / G, h = g * G + rr % G;
-                v[u] = *reinterpret_cast<const uint4*>(p.q + (((size_t)pc.b * a.n + i) * p.Hq + h) * D + at * 64 +
+                v[u] = *reinterpret_cast<const uint4*>(p.q + (((size_t)node0 + i) * p.Hq + h) * D + at * 64 +
                                                        cc * 8);
               }
             }
@@ -552,7 +639,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
       }
       ++si;
       if (p.block_table != nullptr) {
-        ok = produce_paged<D>(p, a, pc, g, s_base, bars, abort, &tm_k, &tm_v, &tm_kt, &tm_vt, lane, jg);
+        ok = produce_paged<D, MODE>(p, a, pc, g, s_base, bars, abort, &tm_k, &tm_v, &tm_kt, &tm_vt, lane, jg);
       } else if (lane == 0) {
         for (int t = pc.tb; t < pc.te; ++t) {
           const int st = jg % S;
@@ -566,13 +653,17 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
           const uint32_t kdst = s_base + Lay::kStageOff + st * Lay::kStageBytes;
           const uint32_t vdst = kdst + Lay::kKBytes;
           if (t < pc.ptiles) {
-            const int y = (pc.b * a.Hkv + g) * a.Lmax + pc.lo + t * kBN;
+            const bool in_shared = MODE == kModeShared && pc.b == 0;
+            const int seq = MODE == kModeShared ? pc.b - 1 : pc.b;
+            const int y = (in_shared ? g * a.Lshared : (seq * a.Hkv + g) * a.Lmax) + piece_key0<MODE>(pc, t);
+            const CUtensorMap* mk = in_shared ? &tm_ks : &tm_k;
+            const CUtensorMap* mv = in_shared ? &tm_vs : &tm_v;
             for (int at = 0; at < Lay::kAtoms; ++at) {
-              tma_load_2d(kdst + at * Lay::kKVAtomBytes, &tm_k, at * 64, y, fb);
-              tma_load_2d(vdst + at * Lay::kKVAtomBytes, &tm_v, at * 64, y, fb);
+              tma_load_2d(kdst + at * Lay::kKVAtomBytes, mk, at * 64, y, fb);
+              tma_load_2d(vdst + at * Lay::kKVAtomBytes, mv, at * 64, y, fb);
             }
           } else {
-            const int z = pc.b * a.n + (t - pc.ptiles) * kBN;
+            const int z = node0 + (t - pc.ptiles) * kBN;
             for (int at = 0; at < Lay::kAtoms; ++at) {
               tma_load_3d(kdst + at * Lay::kKVAtomBytes, &tm_kt, at * 64, g, z, fb);
               tma_load_3d(vdst + at * Lay::kKVAtomBytes, &tm_vt, at * 64, g, z, fb);
@@ -615,7 +706,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
         const uint64_t db = smem_desc(s_base + Lay::kStageOff + (S - 1) * Lay::kStageBytes, 16, 1024, kSwizzle128B);
         mma_bf16_ss(tmem + Lay::kColS + 2u * kBN, da, db, id_qk, 0u);
       }
-      PieceCursor qc, pcur;
+      PieceCursor<MODE> qc, pcur;
       qc.init(bars);
       pcur.init(bars);
       Piece qp, pp;
@@ -717,7 +808,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
     if (p.early) {
       griddep_wait();  // mask and pos come from the previous kernel
       griddep_launch_dependents();
-      if (s_have) row_issue(src, spc, p, r_local, lane, G);
+      if (s_have) row_issue<MODE>(src, spc, p, r_local, lane, G);
     }
     Piece pc = spc;
     RowCtx rc = src;
@@ -731,8 +822,10 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
       Piece pn;
       RowCtx rn;
       const bool have_next = scur.next(a, pn);
-      if (have_next) row_issue(rn, pn, p, r_local, lane, G);  // in flight during this piece
-      const int g = pc.hr / a.RG, rg = pc.hr % a.RG;
+      if (have_next) row_issue<MODE>(rn, pn, p, r_local, lane, G);  // in flight during this piece
+      const int RG = geom_rg<MODE>(a, pc.b);
+      const int g = pc.hr / RG, rg = pc.hr % RG;
+      const int rows = geom_nodes<MODE>(a, pc.b) * G;
       const int row0 = rg * kRowsPerCta;
       const int r_glob = row0 + r_local;
       const bool row_ok = r_glob < rows;
@@ -748,34 +841,55 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
           ok = false;
           break;
         }
+        if (MODE != kModePlain) {
+          // Values of keys that no row sees (past the prefix, between sinks and
+          // window, another sequence's tree) may be anything, NaN included, and
+          // 0 x NaN is NaN: this half's such rows of V are zeroed before P says
+          // that PV may read them.  Only a range's first or last tile has any.
+          const bool tree = t >= pc.ptiles;
+          const int key0 = (tree ? (t - pc.ptiles) * kBN : piece_key0<MODE>(pc, t)) + half * 32;
+          uint32_t seen = low_bits((tree ? a.n : pc.L) - key0);
+          if (MODE == kModeSinks && !tree) seen &= ~low_bits(pc.L - a.window + 1 - key0) | low_bits(a.sinks - key0);
+          if (seen != 0xffffffffu) {  // the same in every warp of the half
+            unsigned char* v = smem + Lay::kStageOff + (jg % S) * Lay::kStageBytes + Lay::kKBytes + half * 32 * 128;
+            for (int e = r_local; e < 32 * Lay::kAtoms * 8; e += 128) {
+              const int key = e / (Lay::kAtoms * 8), piece = e % (Lay::kAtoms * 8);
+              if (!((seen >> key) & 1u))
+                *reinterpret_cast<uint4*>(v + (piece / 8) * Lay::kKVAtomBytes + key * 128 + (piece % 8) * 16) =
+                    make_uint4(0, 0, 0, 0);
+            }
+            fence_proxy_async_smem();
+          }
+        }
         if (warp_live) {
           tc_fence_after();
           float x[32];
           tmem_ld32(t_s + (uint32_t)(sbuf * kBN), x);
           tmem_wait_ld();
           const bool tree = t >= pc.ptiles;
-          const int key0 = (tree ? (t - pc.ptiles) * kBN : pc.lo + t * kBN) + half * 32;
+          const int key0 = (tree ? (t - pc.ptiles) * kBN : piece_key0<MODE>(pc, t)) + half * 32;
           const int k1 = tree ? a.n : pc.L;
           // visibility of this half's 32 keys as one bit mask, built the same
           // way on every tile (so the code stays hot in the instruction cache):
           // keys below the piece's end, then the ancestor bits (tree keys) or
           // the window's lower bound (prefix keys)
           const int lim = k1 - key0;
-          uint32_t vm = lim >= 32 ? 0xffffffffu : (lim > 0 ? (1u << lim) - 1u : 0u);
+          uint32_t vm = low_bits(lim);
           const uint64_t mw = key0 >= 64 ? rc.mw1 : rc.mw0;
           const uint32_t tree_bits = (uint32_t)(mw >> (key0 & 63));
           const int lo_cut = win_lo - key0;  // prefix keys below it are outside the window
-          const uint32_t win_bits =
-              (a.window == 0 || lo_cut <= 0) ? 0xffffffffu : (lo_cut >= 32 ? 0u : ~((1u << lo_cut) - 1u));
+          uint32_t win_bits =
+              (MODE == kModeShared || a.window == 0 || lo_cut <= 0) ? 0xffffffffu : (lo_cut >= 32 ? 0u : ~((1u << lo_cut) - 1u));
+          if (MODE == kModeSinks) win_bits |= low_bits(a.sinks - key0);
           vm &= tree ? tree_bits : win_bits;
           if (!row_ok) vm = 0u;
-          if (tree && a.window > 0) {  // the window on tree keys' positions (rare; warp-uniform)
+          if (MODE != kModeShared && tree && a.window > 0) {  // the window on tree keys' positions (rare; warp-uniform)
             const int grp = key0 >> 5;
             const int tsel = grp == 0 ? rc.tpos[0] : grp == 1 ? rc.tpos[1] : grp == 2 ? rc.tpos[2] : rc.tpos[3];
 #pragma unroll
             for (int cc = 0; cc < 32; ++cc) {
               const int kpos = __shfl_sync(kFull, tsel, cc);  // every lane takes part
-              if (kpos < win_lo) vm &= ~(1u << cc);
+              if (kpos < win_lo && !(MODE == kModeSinks && kpos < a.sinks)) vm &= ~(1u << cc);
             }
           }
           if (__any_sync(kFull, vm != 0xffffffffu)) {  // most prefix tiles see every key
@@ -864,7 +978,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
         const float Ltot = la * wa + lb * wb;
         const float inv = Ltot > 0.f ? 1.f / Ltot : 0.f;
         const float fa = wa * inv, fb = wb * inv;
-        const size_t slot = (size_t)c + (size_t)pc.b * HR + pc.hr;
+        const size_t slot = (size_t)c + (size_t)geom_unit<MODE>(a, pc.b, pc.hr);
         for (int c0 = half * (D / 2); c0 < (half + 1) * (D / 2); c0 += 16) {  // 16 columns at a time
           float oa[16], ob[16];
           tmem_ld16(t_oa + c0, oa);
@@ -874,7 +988,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
 #pragma unroll
           for (int u = 0; u < 16; ++u) oa[u] = fmaf(oa[u], fa, ob[u] * fb);
           if (pc.whole) {
-            __nv_bfloat16* dst = p.out + (((size_t)pc.b * a.n + qi) * p.Hq + qh) * D + c0;
+            __nv_bfloat16* dst = p.out + (((size_t)geom_node0<MODE>(a, pc.b) + qi) * p.Hq + qh) * D + c0;
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
               uint32_t w[4];
@@ -915,7 +1029,9 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
 // each lane loads its D/32 dims of every piece's partial in one round of
 // independent L2 reads, up to kCombChunk pieces at a time, merged online.
 // A unit finished inside one CTA is skipped.  Block (0, 0) also folds the
-// per-CTA status words into the workspace header.
+// per-CTA status words into the workspace header.  In kModeShared the units
+// are the sequences' own, every one left partials, and a row also takes the
+// pieces of the shared unit that holds it.
 constexpr int kCombineWarps = kCombineThreads / 32;
 constexpr int kCombChunk = 8;
 
@@ -929,56 +1045,16 @@ struct CombParams {
   int Hq;
 };
 
+// The pieces c_first..c_last of one unit (its slots start at c_first + unit),
+// row r of its 128, folded into the running (M, wsum, acc).
 template <int D>
-__global__ void __launch_bounds__(kCombineThreads)
-attn_combine_kernel(const CombParams p) {
-  const AttnGeom& a = p.geo;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int HR = a.Hkv * a.RG;
-  const int u = blockIdx.x, b = u / HR, hr = u % HR;
-  const int g = hr / a.RG, rg = hr % a.RG;
-  const int G = p.Hq / a.Hkv;
-  __shared__ long long s_T;
-  __shared__ int s_cfirst, s_clast, s_stat[kCombineWarps];
-  if (warp == 0) {  // the schedule depends only on prefix_len, not on the attention kernel
-    const long long T = geom_prefix(a, a.B, lane);
-    const long long cum = geom_prefix(a, b, lane);
-    const int tiles = geom_tiles(a, b);
-    if (lane == 0) {  // (64-bit divisions: done before the wait, while the attention runs)
-      const long long start = cum + (long long)hr * tiles;
-      s_T = T;
-      s_cfirst = cta_of_tile(start, T, a.C);
-      s_clast = cta_of_tile(start + tiles - 1, T, a.C);
-    }
-  }
-  __syncthreads();
-  griddep_wait();
-  griddep_launch_dependents();  // the next kernel's prologue may overlap this one
-  if (blockIdx.x == 0 && blockIdx.y == 0) {
-    int st = 0;
-    for (int i = tid; i < a.C; i += kCombineThreads) st = max(st, p.cta_status[i]);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) st = max(st, __shfl_xor_sync(kFull, st, o));
-    if (lane == 0) s_stat[warp] = st;
-    __syncthreads();
-    if (tid == 0) {
-      for (int w = 0; w < kCombineWarps; ++w) st = max(st, s_stat[w]);
-      *p.status = st;
-    }
-  }
-  const long long T = s_T;
-  const int c_first = s_cfirst, c_last = s_clast;
-  const bool all_live = T >= a.C;  // with at least one tile per CTA no range is empty
-  const int r = blockIdx.y * kCombineWarps + warp;
-  const int valid = min(kRowsPerCta, a.n * G - rg * kRowsPerCta);
-  if (c_first == c_last || r >= valid) return;
-  const int nseg = c_last - c_first + 1;
-  const size_t slot0 = (size_t)c_first + u;
+__device__ __forceinline__ void combine_pieces(const CombParams& p, long long T, int unit, int c_first, int c_last, int r,
+                                               int lane, float& M, float& wsum, float (&acc)[D / 32]) {
   constexpr int DPL = D / 32;  // output dims per lane
-  float M = -INFINITY, wsum = 0.f;
-  float acc[DPL];
-#pragma unroll
-  for (int t = 0; t < DPL; ++t) acc[t] = 0.f;
+  const int C = p.geo.C;
+  const bool all_live = T >= C;  // with at least one tile per CTA no range is empty
+  const int nseg = c_last - c_first + 1;
+  const size_t slot0 = (size_t)c_first + unit;
   for (int s0 = 0; s0 < nseg; s0 += kCombChunk) {
     float ls[kCombChunk];
     float v[kCombChunk][DPL];
@@ -987,7 +1063,7 @@ attn_combine_kernel(const CombParams p) {
       // a CTA with an empty range wrote no partial: read the first piece's
       // (always written, finite) and give it weight 0
       const int s = s0 + j;
-      const bool live = s < nseg && (all_live || cta_nonempty(c_first + s, T, a.C));
+      const bool live = s < nseg && (all_live || cta_nonempty(c_first + s, T, C));
       const size_t sl = live ? slot0 + s : slot0;
       ls[j] = live ? __ldcg(p.part_lse + sl * kRowsPerCta + r) : -INFINITY;
       const float* src = p.part_o + (sl * kRowsPerCta + r) * D + lane * DPL;
@@ -1016,7 +1092,71 @@ attn_combine_kernel(const CombParams p) {
     }
     M = mc;
   }
+}
+
+template <int D, int MODE>
+__global__ void __launch_bounds__(kCombineThreads)
+attn_combine_kernel(const CombParams p) {
+  const AttnGeom& a = p.geo;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int HR = a.Hkv * a.RG;
+  const int u = blockIdx.x, b = u / HR, hr = u % HR;
+  const int sb = MODE == kModeShared ? b + 1 : b;  // the schedule's sequence
+  const int g = hr / a.RG, rg = hr % a.RG;
+  const int G = p.Hq / a.Hkv;
+  const int r = blockIdx.y * kCombineWarps + warp;
   const int row = rg * kRowsPerCta + r;
+  __shared__ long long s_T;
+  __shared__ int s_cfirst, s_clast, s_stat[kCombineWarps];
+  if (warp == 0) {  // the schedule depends only on prefix_len, not on the attention kernel
+    const long long T = geom_prefix<MODE>(a, geom_seqs<MODE>(a), lane);
+    const long long cum = geom_prefix<MODE>(a, sb, lane);
+    const int tiles = geom_tiles<MODE>(a, sb);
+    if (lane == 0) {  // (64-bit divisions: done before the wait, while the attention runs)
+      const long long start = cum + (long long)hr * tiles;
+      s_T = T;
+      s_cfirst = cta_of_tile(start, T, a.C);
+      s_clast = cta_of_tile(start + tiles - 1, T, a.C);
+    }
+  }
+  __syncthreads();
+  const long long T = s_T;
+  const int c_first = s_cfirst, c_last = s_clast;
+  // kModeShared: the shared unit, CTAs and row that hold this warp's row
+  int us = 0, us_first = 0, us_last = -1, rs = 0;
+  if (MODE == kModeShared) {
+    const int tiles = geom_tiles<MODE>(a, 0);
+    const int at = b * a.n * G + row;
+    us = g * a.RGs + at / kRowsPerCta;
+    rs = at % kRowsPerCta;
+    if (tiles > 0 && row < a.n * G) {
+      us_first = cta_of_tile((long long)us * tiles, T, a.C);
+      us_last = cta_of_tile((long long)us * tiles + tiles - 1, T, a.C);
+    }
+  }
+  griddep_wait();
+  griddep_launch_dependents();  // the next kernel's prologue may overlap this one
+  if (blockIdx.x == 0 && blockIdx.y == 0) {
+    int st = 0;
+    for (int i = tid; i < a.C; i += kCombineThreads) st = max(st, p.cta_status[i]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) st = max(st, __shfl_xor_sync(kFull, st, o));
+    if (lane == 0) s_stat[warp] = st;
+    __syncthreads();
+    if (tid == 0) {
+      for (int w = 0; w < kCombineWarps; ++w) st = max(st, s_stat[w]);
+      *p.status = st;
+    }
+  }
+  const int valid = min(kRowsPerCta, a.n * G - rg * kRowsPerCta);
+  if ((MODE != kModeShared && c_first == c_last) || r >= valid) return;
+  constexpr int DPL = D / 32;  // output dims per lane
+  float M = -INFINITY, wsum = 0.f;
+  float acc[DPL];
+#pragma unroll
+  for (int t = 0; t < DPL; ++t) acc[t] = 0.f;
+  if (MODE == kModeShared && us_last >= us_first) combine_pieces<D>(p, T, us, us_first, us_last, rs, lane, M, wsum, acc);
+  combine_pieces<D>(p, T, geom_unit<MODE>(a, sb, hr), c_first, c_last, r, lane, M, wsum, acc);
   const int i = row / G, h = g * G + row % G;
   __nv_bfloat16* dst = p.out + (((size_t)b * a.n + i) * p.Hq + h) * D + lane * DPL;
   const float inv = wsum > 0.f ? 1.f / wsum : 0.f;
@@ -1055,23 +1195,22 @@ bool make_map(CUtensorMap* m, const void* base, int rank, const cuuint64_t* dims
 
 }  // namespace
 
-template <int D>
-static cudaError_t launch_tc(const void* q, const void* kc, const void* vc, const int32_t* plen, int Lmax,
-                             const void* kt, const void* vt, const uint64_t* mask, const int32_t* pos, int B,
-                             int n, int Hq, int Hkv, int window, float scale, void* out, void* ws, cudaStream_t s,
-                             const PagedKV* pg, bool early) {
-  CUtensorMap mk, mv, mkt, mvt;
+template <int D, int MODE>
+static cudaError_t launch_tc(const AttnCall& k, cudaStream_t s) {
+  const PagedKV* pg = k.pg;
+  const int B = k.B, n = k.n, Hq = k.Hq, Hkv = k.Hkv;
+  CUtensorMap mk, mv, mkt, mvt, mks, mvs;
   const bool paged = pg != nullptr && pg->block_table != nullptr;
-  if (paged) Lmax = pg->pages_per_seq * pg->page_size;  // a sequence's capacity
+  const int Lmax = paged ? pg->pages_per_seq * pg->page_size : k.Lmax;  // a sequence's capacity
   const int Lrows = Lmax > 0 ? Lmax : 1;
-  const void* kbase = Lmax > 0 ? kc : kt;  // any valid address when the cache is empty
-  const void* vbase = Lmax > 0 ? vc : vt;
+  const void* kbase = Lmax > 0 ? k.kc : k.kt;  // any valid address when the cache is empty
+  const void* vbase = Lmax > 0 ? k.vc : k.vt;
   if (paged) {
     // pools [num_pages][Hkv][page_size][D] as rows of D; a box is min(page_size, 64) keys
     const cuuint64_t dims[2] = {(cuuint64_t)D, (cuuint64_t)pg->num_pages * Hkv * pg->page_size};
     const cuuint64_t str[1] = {(cuuint64_t)D * 2};
     const cuuint32_t box[2] = {64, (cuuint32_t)(pg->page_size < kBN ? pg->page_size : kBN)};
-    if (!make_map(&mk, kc, 2, dims, str, box) || !make_map(&mv, vc, 2, dims, str, box)) return cudaErrorInvalidValue;
+    if (!make_map(&mk, k.kc, 2, dims, str, box) || !make_map(&mv, k.vc, 2, dims, str, box)) return cudaErrorInvalidValue;
   } else {
     const cuuint64_t dims[2] = {(cuuint64_t)D, (cuuint64_t)B * Hkv * Lrows};
     const cuuint64_t str[1] = {(cuuint64_t)D * 2};
@@ -1085,8 +1224,16 @@ static cudaError_t launch_tc(const void* q, const void* kc, const void* vc, cons
     const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)Hkv, (cuuint64_t)B * n};
     const cuuint64_t str[2] = {(cuuint64_t)D * 2, (cuuint64_t)Hkv * D * 2};
     const cuuint32_t box[3] = {64, 1, (cuuint32_t)kBN};
-    if (!make_map(&mkt, kt, 3, dims, str, box) || !make_map(&mvt, vt, 3, dims, str, box))
+    if (!make_map(&mkt, k.kt, 3, dims, str, box) || !make_map(&mvt, k.vt, 3, dims, str, box))
       return cudaErrorInvalidValue;
+  }
+  mks = mk;
+  mvs = mv;
+  if (MODE == kModeShared && !paged && k.Lshared > 0) {
+    const cuuint64_t dims[2] = {(cuuint64_t)D, (cuuint64_t)Hkv * k.Lshared};
+    const cuuint64_t str[1] = {(cuuint64_t)D * 2};
+    const cuuint32_t box[2] = {64, (cuuint32_t)kBN};
+    if (!make_map(&mks, k.ks, 2, dims, str, box) || !make_map(&mvs, k.vs, 2, dims, str, box)) return cudaErrorInvalidValue;
   }
   const int G = Hq / Hkv;
   CUtensorMap mq;
@@ -1095,38 +1242,45 @@ static cudaError_t launch_tc(const void* q, const void* kc, const void* vc, cons
     const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)Hq, (cuuint64_t)B * n};
     const cuuint64_t str[2] = {(cuuint64_t)D * 2, (cuuint64_t)Hq * D * 2};
     const cuuint32_t box[3] = {64, (cuuint32_t)(q_tma ? G : 1), (cuuint32_t)(q_tma ? kRowsPerCta / G : 1)};
-    if (!make_map(&mq, q, 3, dims, str, box)) return cudaErrorInvalidValue;
+    if (!make_map(&mq, k.q, 3, dims, str, box)) return cudaErrorInvalidValue;
   }
-  const AttnWorkspace wl = attention_ws_layout(B, n, Hq, Hkv, D, Lmax, window);
-  unsigned char* wsb = static_cast<unsigned char*>(ws);
+  const AttnShape shape = {B, n, Hq, Hkv, D, Lmax, k.window, k.sinks, k.Lshared};
+  const AttnWorkspace wl = attention_ws_layout(shape);
+  unsigned char* wsb = static_cast<unsigned char*>(k.ws);
   TcParams p;
-  p.q = static_cast<const __nv_bfloat16*>(q);
-  p.mask = mask;
-  p.pos = pos;
-  p.out = static_cast<__nv_bfloat16*>(out);
+  p.q = static_cast<const __nv_bfloat16*>(k.q);
+  p.mask = k.mask;
+  p.pos = k.pos;
+  p.out = static_cast<__nv_bfloat16*>(k.out);
   p.part_o = reinterpret_cast<float*>(wsb + wl.part_o_off);
   p.part_lse = reinterpret_cast<float*>(wsb + wl.part_lse_off);
   p.cta_status = reinterpret_cast<int*>(wsb + wl.cta_status_off);
-  p.geo.plen = plen;
+  p.geo.plen = k.plen;
   p.geo.B = B;
   p.geo.Hkv = Hkv;
   p.geo.RG = attention_row_groups(n, Hq, Hkv);
   p.geo.n = n;
   p.geo.Lmax = Lmax;
-  p.geo.window = window;
-  p.geo.C = attention_ctas(B, n, Hq, Hkv, Lmax, window);
+  p.geo.window = k.window;
+  p.geo.C = attention_ctas(shape);
   p.geo.lo_align = paged ? kBN : 1;
+  p.geo.sinks = k.sinks;
+  p.geo.shared_len = k.shared_len;
+  p.geo.Lshared = k.Lshared;
+  p.geo.RGs = MODE == kModeShared ? attention_shared_row_groups(shape) : 0;
   p.Hq = Hq;
   p.block_table = paged ? pg->block_table : nullptr;
   p.page_size = paged ? pg->page_size : 0;
   p.pages_per_seq = paged ? pg->pages_per_seq : 0;
   p.num_pages = paged ? pg->num_pages : 0;
+  p.shared_table = k.shared_table;
+  p.shared_pages = k.shared_pages;
   p.q_by_tma = q_tma ? 1 : 0;
-  p.scale_log2 = scale * 1.4426950408889634f;
+  p.scale_log2 = k.scale * 1.4426950408889634f;
   p.probe_ns = attention_wait_probe_ns();
-  p.early = early ? 1 : 0;
+  p.early = k.early ? 1 : 0;
   const size_t smem = TcLayout<D>::kSmemBytes;
-  cudaError_t e = ensure_smem_limit((const void*)attn_tc_kernel<D>, smem);
+  cudaError_t e = ensure_smem_limit((const void*)attn_tc_kernel<D, MODE>, smem);
   if (e != cudaSuccess) return e;
 
   // both kernels may start while their predecessor drains (programmatic
@@ -1141,7 +1295,7 @@ static cudaError_t launch_tc(const void* q, const void* kc, const void* vc, cons
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, attn_tc_kernel<D>, mk, mv, mkt, mvt, mq, p);
+  e = cudaLaunchKernelEx(&cfg, attn_tc_kernel<D, MODE>, mk, mv, mkt, mvt, mq, mks, mvs, p);
   if (e != cudaSuccess) return e;
 
   CombParams cp;
@@ -1159,17 +1313,15 @@ static cudaError_t launch_tc(const void* q, const void* kc, const void* vc, cons
   cfg2.stream = s;
   cfg2.attrs = attr;
   cfg2.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg2, attn_combine_kernel<D>, cp);
+  return cudaLaunchKernelEx(&cfg2, attn_combine_kernel<D, MODE>, cp);
 }
 
-cudaError_t launch_tree_attention(const void* q, const void* kc, const void* vc, const int32_t* plen, int Lmax,
-                                  const void* kt, const void* vt, const uint64_t* mask, const int32_t* pos, int B,
-                                  int n, int Hq, int Hkv, int D, int window, float scale, void* out, void* ws,
-                                  cudaStream_t s, const PagedKV* pg, bool early) {
-  if (D == 128)
-    return launch_tc<128>(q, kc, vc, plen, Lmax, kt, vt, mask, pos, B, n, Hq, Hkv, window, scale, out, ws, s, pg,
-                          early);
-  return launch_tc<64>(q, kc, vc, plen, Lmax, kt, vt, mask, pos, B, n, Hq, Hkv, window, scale, out, ws, s, pg, early);
+cudaError_t launch_tree_attention(const AttnCall& k, cudaStream_t s) {
+  if (k.shared_len != nullptr) return k.D == 128 ? launch_tc<128, kModeShared>(k, s) : launch_tc<64, kModeShared>(k, s);
+  // without a window every key is visible and the sinks change nothing
+  if (k.sinks > 0 && k.window > 0)
+    return k.D == 128 ? launch_tc<128, kModeSinks>(k, s) : launch_tc<64, kModeSinks>(k, s);
+  return k.D == 128 ? launch_tc<128, kModePlain>(k, s) : launch_tc<64, kModePlain>(k, s);
 }
 
 }  // namespace eagle

@@ -111,27 +111,52 @@ int attention_row_groups(int n, int Hq, int Hkv);
 // The wait probe's limit for the next attention launches (0: off); see
 // eagle_debug_attention_wait_probe.
 unsigned long long attention_wait_probe_ns();
-int attention_ctas(int B, int n, int Hq, int Hkv, int Lmax, int window);  // C
-AttnWorkspace attention_ws_layout(int B, int n, int Hq, int Hkv, int D, int Lmax, int window);
-inline size_t attention_ws_bytes(int B, int n, int Hq, int Hkv, int D, int Lmax, int window) {
-  return attention_ws_layout(B, n, Hq, Hkv, D, Lmax, window).bytes;
-}
+// What the schedule and the workspace depend on.
+struct AttnShape {
+  int B, n, Hq, Hkv, D, Lmax, window;
+  int sinks;    // first keys that stay visible under the window (0: none)
+  int Lshared;  // capacity of the prefix that the batch shares (0: none)
+};
+int attention_shared_row_groups(const AttnShape& a);  // row groups of the whole batch (0 without shared keys)
+int attention_ctas(const AttnShape& a);                // C
+AttnWorkspace attention_ws_layout(const AttnShape& a);
+inline size_t attention_ws_bytes(const AttnShape& a) { return attention_ws_layout(a).bytes; }
 // A paged prefix cache: pools [num_pages][Hkv][page_size][D], block_table
 // [B][pages_per_seq] page ids; page_size is 16, 32 or a multiple of 64.
 struct PagedKV {
   const int32_t* block_table;
   int page_size, pages_per_seq, num_pages;
 };
-// pg == nullptr: dense caches [B][Hkv][Lmax][D]; else kc / vc are the pools
-// and a sequence holds up to pages_per_seq * page_size keys (Lmax unused).
-// early: every input except mask and pos was complete before the previous
-// kernel on the stream started, so the K/V stream begins before that kernel
-// ends (only the fused step, whose previous kernel is the expansion, sets it).
-cudaError_t launch_tree_attention(const void* q, const void* kc, const void* vc, const int32_t* plen,
-                                  int Lmax, const void* kt, const void* vt, const uint64_t* mask,
-                                  const int32_t* pos, int B, int n, int Hq, int Hkv, int D, int window,
-                                  float scale, void* out, void* ws, cudaStream_t s, const PagedKV* pg = nullptr,
-                                  bool early = false);
+// One tree attention.
+//   pg == nullptr: dense caches [B][Hkv][Lmax][D]; else kc / vc are the pools
+//     and a sequence holds up to pages_per_seq * page_size keys (Lmax unused).
+//   early: every input except mask and pos was complete before the previous
+//     kernel on the stream started, so the K/V stream begins before that kernel
+//     ends (only the fused step, whose previous kernel is the expansion, sets it).
+//   sinks: keys below it stay visible under a window.
+//   shared_len != nullptr: all sequences share *shared_len (clamped to
+//     [0, Lshared]) keys before their own: ks / vs [Hkv][Lshared][D], or with
+//     pg the pages of shared_table [shared_pages]; no window.
+struct AttnCall {
+  const void *q, *kc, *vc;
+  const int32_t* plen;
+  int Lmax;
+  const void *kt, *vt;
+  const uint64_t* mask;
+  const int32_t* pos;
+  int B, n, Hq, Hkv, D, window;
+  float scale;
+  void *out, *ws;
+  const PagedKV* pg = nullptr;
+  bool early = false;
+  int sinks = 0;
+  const int32_t* shared_len = nullptr;
+  const void *ks = nullptr, *vs = nullptr;
+  int Lshared = 0;
+  const int32_t* shared_table = nullptr;
+  int shared_pages = 0;
+};
+cudaError_t launch_tree_attention(const AttnCall& k, cudaStream_t s);
 
 // ---- KV-cache compaction after acceptance (kv_compact.cu)
 cudaError_t launch_kv_compact(const void* k_tree, const void* v_tree, const int32_t* path, const int32_t* accepted_len,

@@ -26,8 +26,9 @@
  * the EAGLE-4 harness's cost-aware sizing (eagle_cost_at,
  * eagle_size_keep_level); EAGLE-1's static tree (eagle_static_tree_build);
  * sampling without replacement (eagle_accept_with_rule); a paged prefix cache
- * (eagle_tree_attention_paged); and the accepted path's keys and values into
- * the cache (eagle_kv_compact, _paged).
+ * (eagle_tree_attention_paged); a window with sinks (_with_sinks) and a prefix
+ * the batch shares (_shared) in the attention; and the accepted path's keys and
+ * values into the cache (eagle_kv_compact, _paged).
  *
  * Conventions shared by every entry point
  *   - All array arguments are DEVICE pointers owned by the caller, unless a
@@ -224,6 +225,66 @@ EAGLE_API eagle_status eagle_tree_attention_paged(const void* q, const void* k_p
                                                   const void* v_tree, const uint64_t* mask, const int32_t* pos,
                                                   int B, int n, int Hq, int Hkv, int D, int window, float scale,
                                                   void* out, void* workspace, size_t workspace_bytes, void* stream);
+
+/* --------------------------------------- window with sinks, tree attention
+ * eagle_tree_attention[_paged] where the first `sinks` keys stay visible under
+ * the window: node i sees prefix entry p iff p >= pos_i - W + 1 or p < sinks,
+ * and tree entry j of its mask iff pos_j >= pos_i - W + 1 or pos_j < sinks.
+ * sinks = 0 is eagle_tree_attention[_paged]; without a window (window = 0) all
+ * keys are visible and sinks changes nothing.  Only the sinks' and the
+ * window's keys are read, so the cost does not grow with the prefix.  With
+ * sinks > 0 and a window, entries that no node sees (between the sinks and the
+ * window, past prefix_len) may hold anything, NaN included, and a paged
+ * cache's pages that hold only such keys may be missing from the block table.
+ * sinks < 0 returns EAGLE_ERR_SHAPE; otherwise as the calls without sinks.
+ * Workspace: eagle_tree_attention_sinks_workspace_bytes (paged: Lmax =
+ * pages_per_seq * page_size). */
+EAGLE_API size_t eagle_tree_attention_sinks_workspace_bytes(int B, int n, int Hq, int Hkv, int D, int Lmax, int window,
+                                                            int sinks);
+EAGLE_API eagle_status eagle_tree_attention_with_sinks(const void* q, const void* k_cache, const void* v_cache,
+                                                       const int32_t* prefix_len, int Lmax, const void* k_tree,
+                                                       const void* v_tree, const uint64_t* mask, const int32_t* pos,
+                                                       int B, int n, int Hq, int Hkv, int D, int window, int sinks,
+                                                       float scale, void* out, void* workspace,
+                                                       size_t workspace_bytes, void* stream);
+EAGLE_API eagle_status eagle_tree_attention_paged_with_sinks(
+    const void* q, const void* k_pages, const void* v_pages, int num_pages, int page_size, const int32_t* block_table,
+    int pages_per_seq, const int32_t* prefix_len, const void* k_tree, const void* v_tree, const uint64_t* mask,
+    const int32_t* pos, int B, int n, int Hq, int Hkv, int D, int window, int sinks, float scale, void* out,
+    void* workspace, size_t workspace_bytes, void* stream);
+
+/* ------------------------------------- shared prefix, tree attention
+ * Tree attention for a batch whose sequences begin with the same keys (a
+ * system prompt, a document): those are held once and read once for the whole
+ * batch.  Node i of sequence b sees the shared entries p < *shared_len, its own
+ * prefix entries p < prefix_len[b] and the tree entries of its mask.
+ *   k_shared, v_shared [Hkv][Lshared][D] bf16 (NULL allowed iff Lshared = 0)
+ *   shared_len [1] int32 device, clamped to [0, Lshared]
+ *   k_cache, v_cache, prefix_len, Lmax: each sequence's own keys after the
+ *     shared ones, as in eagle_tree_attention (prefix_len[b] may be 0)
+ * paged: the shared keys are the pages shared_table [shared_pages] (device) of
+ * the same pools, the key at position p at offset p % page_size of page
+ * shared_table[p / page_size]; a sequence's own keys start on a page of its
+ * own (block_table as in eagle_tree_attention_paged).
+ * Entries past *shared_len and prefix_len[b] may hold anything.  No window.
+ * The result equals attention over the concatenated prefix up to the order of
+ * floating-point sums.  Everything else as in eagle_tree_attention[_paged];
+ * the device status word covers the shared pages as well.  Limit: B * n *
+ * (Hq / Hkv) < 2^31 - 128.  Workspace: eagle_tree_attention_shared_workspace_bytes
+ * (paged: Lshared = shared_pages * page_size, Lmax = pages_per_seq * page_size). */
+EAGLE_API size_t eagle_tree_attention_shared_workspace_bytes(int B, int n, int Hq, int Hkv, int D, int Lshared,
+                                                             int Lmax);
+EAGLE_API eagle_status eagle_tree_attention_shared(const void* q, const void* k_shared, const void* v_shared,
+                                                   int Lshared, const int32_t* shared_len, const void* k_cache,
+                                                   const void* v_cache, const int32_t* prefix_len, int Lmax,
+                                                   const void* k_tree, const void* v_tree, const uint64_t* mask, int B,
+                                                   int n, int Hq, int Hkv, int D, float scale, void* out,
+                                                   void* workspace, size_t workspace_bytes, void* stream);
+EAGLE_API eagle_status eagle_tree_attention_shared_paged(
+    const void* q, const void* k_pages, const void* v_pages, int num_pages, int page_size, const int32_t* shared_table,
+    int shared_pages, const int32_t* shared_len, const int32_t* block_table, int pages_per_seq,
+    const int32_t* prefix_len, const void* k_tree, const void* v_tree, const uint64_t* mask, int B, int n, int Hq,
+    int Hkv, int D, float scale, void* out, void* workspace, size_t workspace_bytes, void* stream);
 
 /* ----------------------------------------------------------------- accept
  * Walk each tree from the root ("EAGLE" notes, EAGLE-2 "Well-Calibrated Draft

@@ -10,7 +10,8 @@ keys are the prefix entries 0..L-1 of KV head h // (Hq/Hkv) followed by the n
 tree entries; the scores q.k * scale over the visible keys go through a
 softmax and weight the values.  Visible: prefix key p iff no window or
 p >= pos_i - W + 1; tree key j iff node j+1 is node i+1 or an ancestor (and,
-with a window, pos_j >= pos_i - W + 1).  scale defaults to 1/sqrt(D).
+with a window, pos_j >= pos_i - W + 1).  With a window, the first `sinks`
+positions stay visible whatever the window.  scale defaults to 1/sqrt(D).
 """
 from __future__ import annotations
 
@@ -22,7 +23,7 @@ import numpy as np
 from .mask import ancestor_mask
 
 
-def _visible(L: int, parents, depth, window: int) -> np.ndarray:
+def _visible(L: int, parents, depth, window: int, sinks: int = 0) -> np.ndarray:
     anc = ancestor_mask(parents)
     n = anc.shape[0]
     pos = L - 1 + np.asarray(depth, dtype=np.int64)
@@ -30,8 +31,9 @@ def _visible(L: int, parents, depth, window: int) -> np.ndarray:
     for i in range(n):
         lo = 0 if window <= 0 else max(0, int(pos[i]) - window + 1)
         vis[i, lo:L] = True
+        vis[i, :min(sinks, L)] = True
         for j in range(n):
-            if anc[i, j] and (window <= 0 or pos[j] >= pos[i] - window + 1):
+            if anc[i, j] and (window <= 0 or pos[j] >= pos[i] - window + 1 or pos[j] < sinks):
                 vis[i, L + j] = True
     return vis
 
@@ -43,7 +45,7 @@ def _softmax_rows(s: np.ndarray) -> np.ndarray:
 
 
 def tree_attention(q, k_cache, v_cache, L: int, k_tree, v_tree, parents, depth,
-                   window: int = 0, scale: Optional[float] = None, return_weights: bool = False):
+                   window: int = 0, scale: Optional[float] = None, return_weights: bool = False, sinks: int = 0):
     """One sequence.  q [n][Hq][D]; k_cache, v_cache [Hkv][>=L][D];
     k_tree, v_tree [n][Hkv][D]; all fp64.  Returns out [n][Hq][D] fp64, and with
     return_weights also the softmax weights [n][Hq][L+n] over (prefix keys,
@@ -53,7 +55,7 @@ def tree_attention(q, k_cache, v_cache, L: int, k_tree, v_tree, parents, depth,
     Hkv = k_cache.shape[0]
     G = Hq // Hkv
     scale = 1.0 / math.sqrt(D) if scale is None else scale
-    vis = _visible(L, parents, depth, window)
+    vis = _visible(L, parents, depth, window, sinks)
     out = np.empty((n, Hq, D), dtype=np.float64)
     weights = np.empty((n, Hq, L + n), dtype=np.float64) if return_weights else None
     for h in range(Hq):
@@ -71,14 +73,14 @@ def tree_attention(q, k_cache, v_cache, L: int, k_tree, v_tree, parents, depth,
 
 def tree_attention_rows(q, k_cache, v_cache, L: int, k_tree, v_tree, parents, depth,
                         rows: Iterable[Tuple[int, int]], window: int = 0,
-                        scale: Optional[float] = None, return_weights: bool = False):
+                        scale: Optional[float] = None, return_weights: bool = False, sinks: int = 0):
     """The same, for selected (node index i, head h) pairs only -> [len(rows)][D]
     (and with return_weights the weights [len(rows)][L+n])."""
     n, Hq, D = q.shape
     Hkv = k_cache.shape[0]
     G = Hq // Hkv
     scale = 1.0 / math.sqrt(D) if scale is None else scale
-    vis = _visible(L, parents, depth, window)
+    vis = _visible(L, parents, depth, window, sinks)
     res, ws = [], []
     for i, h in rows:
         g = h // G
