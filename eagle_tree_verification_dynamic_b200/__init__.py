@@ -13,8 +13,12 @@ preallocated outputs and workspaces, for CUDA-graph capture):
   ``static_tree_build`` fills EAGLE-1's fixed template instead)
 * ``tree_mask``        ancestor bitmask and position ids
 * ``tree_attention``   tree-masked attention over the prefix cache and the tree
-  (``tree_attention_paged`` for a paged cache)
-* ``accept``           greedy or sampled acceptance, with or without replacement
+  (``tree_attention_paged`` for a paged cache; ``sinks`` keeps the first keys
+  visible under a window; ``tree_attention_shared`` and ``_shared_paged`` for a
+  batch whose sequences begin with the same keys)
+* ``accept``           greedy or sampled acceptance, with or without replacement,
+  under the requests' ``Sampling`` parameters (temperature, top-k, top-p, min-p)
+* ``sample``           a token per logit row under the same parameters
 * ``kv_compact``       the accepted path's keys and values into the cache
   (``kv_compact_paged``)
 
@@ -26,6 +30,7 @@ from ._lib import (  # noqa: F401
     BF16,
     F32,
     EagleError,
+    Sampling,
     Tree,
     TreeGrower,
     accept,
@@ -43,12 +48,15 @@ from ._lib import (  # noqa: F401
     lib,
     pool_size,
     row_stats,
+    sample,
+    sample_into,
     shared_attention_workspace_bytes,
     static_template_from_paths,
     static_tree_build,
     static_tree_rows,
     step_in,
     step_into,
+    step_options,
     step_workspace_bytes,
     tree_attention,
     tree_attention_into,

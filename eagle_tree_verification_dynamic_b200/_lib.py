@@ -45,6 +45,14 @@ class StepIn(ctypes.Structure):
                 ("block_table", _c_p), ("page_size", _c_i), ("pages_per_seq", _c_i), ("num_pages", _c_i)]
 
 
+class SamplingStruct(ctypes.Structure):
+    _fields_ = [("temperature", _c_p), ("top_k", _c_p), ("top_p", _c_p), ("min_p", _c_p)]
+
+
+class StepOptions(ctypes.Structure):
+    _fields_ = [("sinks", _c_i), ("sampling", ctypes.POINTER(SamplingStruct))]
+
+
 class CostTableStruct(ctypes.Structure):
     _fields_ = [("nB", _c_i), ("nL", _c_i), ("nN", _c_i), ("B", _c_p), ("L", _c_p), ("N", _c_p), ("us", _c_p)]
 
@@ -117,6 +125,14 @@ _SIGS = {
     "eagle_accept_workspace_bytes": (_c_sz, [_c_i, _c_i, _c_i, _c_i]),
     "eagle_accept_with_rule": (_c_i, [_c_p, _c_i, _c_p, _c_i, _c_p, _c_i, _c_p, _c_p, _c_p, _c_p, _c_i, _c_i, _c_i,
                                       _c_i, _c_i, _c_p, _c_p, _c_p, _c_p, _c_sz, _c_p]),
+    "eagle_sample": (_c_i, [_c_p, _c_i, _c_ll, _c_i, _c_ll, ctypes.POINTER(SamplingStruct), _c_p, _c_p, _c_p, _c_p]),
+    "eagle_accept_with_sampling": (_c_i, [_c_p, _c_i, _c_p, _c_i, _c_p, _c_i, _c_p, _c_p, _c_p, _c_p, _c_i,
+                                          ctypes.POINTER(SamplingStruct), _c_i, _c_i, _c_i, _c_i, _c_p, _c_p, _c_p,
+                                          _c_p, _c_sz, _c_p]),
+    "eagle_verify_step_options_workspace_bytes": (_c_sz, [ctypes.POINTER(StepIn), ctypes.POINTER(StepOptions)]),
+    "eagle_verify_step_options_attention_status_offset": (_c_sz, [ctypes.POINTER(StepIn), ctypes.POINTER(StepOptions)]),
+    "eagle_verify_step_with_options": (_c_i, [ctypes.POINTER(StepIn), ctypes.POINTER(StepOptions),
+                                              ctypes.POINTER(StepOut), ctypes.POINTER(_c_i), _c_p, _c_sz, _c_p]),
     "eagle_accept": (_c_i, [_c_p, _c_i, _c_p, _c_i, _c_p, _c_i, _c_p, _c_p, _c_p, _c_p, _c_i, _c_i,
                             _c_i, _c_i, _c_p, _c_p, _c_p, _c_p, _c_sz, _c_p]),
 }
@@ -492,13 +508,72 @@ def accept_workspace_bytes(B, n, V, dtype_code) -> int:
 SAMPLE_WITH_REPLACEMENT, SAMPLE_WITHOUT_REPLACEMENT = 0, 1
 
 
+@dataclass
+class Sampling:
+    """What requests ask of their samples: device tensors with one entry per row (for accept and the step: per
+    sequence), None = off.  temperature f32 (<= 0: greedy), top_k int32 (<= 0: off), top_p f32 (>= 1: off), min_p f32
+    (<= 0: off)."""
+    temperature: Optional[torch.Tensor] = None
+    top_k: Optional[torch.Tensor] = None
+    top_p: Optional[torch.Tensor] = None
+    min_p: Optional[torch.Tensor] = None
+
+    def struct(self) -> SamplingStruct:
+        return SamplingStruct(_ptr(self.temperature), _ptr(self.top_k), _ptr(self.top_p), _ptr(self.min_p))
+
+    def check(self, rows: int, like: torch.Tensor):
+        """Raise unless every given tensor has `rows` entries of its type on `like`'s device."""
+        for name, dt in (("temperature", torch.float32), ("top_k", torch.int32), ("top_p", torch.float32),
+                         ("min_p", torch.float32)):
+            t = getattr(self, name)
+            if t is None:
+                continue
+            _need_cuda(like.detach()[:0].reshape(-1), t)
+            if t.dtype != dt or t.numel() != rows:
+                raise EagleError(f"sampling: {name} must be {rows} x {dt}")
+
+
+def sample_into(logits, uniforms, sampling: Optional[Sampling], tokens, logprob=None):
+    """eagle_sample into preallocated tokens [rows] int32 and logprob [rows] f32 (or None)."""
+    rows, V = logits.shape
+    st = None if sampling is None else ctypes.byref(sampling.struct())
+    _check(lib().eagle_sample(_ptr(logits), _dtype_code(logits), rows, V, logits.stride(0) if rows > 1 else V, st,
+                              _ptr(uniforms), _ptr(tokens), _ptr(logprob), _stream(logits.device)), "eagle_sample")
+
+
+def sample(logits: torch.Tensor, uniforms: torch.Tensor, sampling: Optional[Sampling] = None):
+    """A token per row of logits [rows][V] (f32 or bf16; rows may be strided, e.g. logits[:, -1]) from uniforms
+    [rows] f32 in [0, 1), under the rows' sampling parameters -> (tokens [rows] int32, logprob [rows] f32)."""
+    if logits.dim() != 2 or not logits.is_cuda or (logits.shape[1] > 1 and logits.stride(1) != 1):
+        raise EagleError("logits must be [rows][V] on a CUDA device, each row contiguous")
+    rows = logits.shape[0]
+    if rows > 1 and logits.stride(0) < logits.shape[1]:
+        raise EagleError("logits: rows overlap")
+    _need_cuda(logits[:0].reshape(-1), uniforms)
+    if uniforms.dtype != torch.float32 or uniforms.numel() != rows:
+        raise EagleError(f"uniforms must be {rows} x float32")
+    if sampling is not None:
+        sampling.check(rows, logits)
+    tokens = torch.empty(rows, dtype=torch.int32, device=logits.device)
+    logprob = torch.empty(rows, dtype=torch.float32, device=logits.device)
+    sample_into(logits, uniforms, sampling, tokens, logprob)
+    return tokens, logprob
+
+
 def accept_into(target_logits, tokens, parents, draft_row, depth, uniforms, draft_logits, draft_lse,
-                accepted_len, path, bonus, ws, without_replacement: bool = False):
+                accepted_len, path, bonus, ws, without_replacement: bool = False, sampling: Optional[Sampling] = None):
     B, n1, V = target_logits.shape
     n = n1 - 1
     R = draft_logits.shape[1] if draft_logits is not None else 0
     ddt = _dtype_code(draft_logits) if draft_logits is not None else 0
     rule = SAMPLE_WITHOUT_REPLACEMENT if without_replacement else SAMPLE_WITH_REPLACEMENT
+    if sampling is not None:
+        _check(lib().eagle_accept_with_sampling(
+            _ptr(target_logits), _dtype_code(target_logits), _ptr(draft_logits), ddt, _ptr(draft_lse), R, _ptr(tokens),
+            _ptr(parents), _ptr(draft_row), _ptr(uniforms), rule, ctypes.byref(sampling.struct()), B, n, V, depth,
+            _ptr(accepted_len), _ptr(path), _ptr(bonus), _ptr(ws), ws.numel(), _stream(target_logits.device)),
+            "eagle_accept_with_sampling")
+        return
     _check(lib().eagle_accept_with_rule(_ptr(target_logits), _dtype_code(target_logits), _ptr(draft_logits), ddt,
                                         _ptr(draft_lse), R, _ptr(tokens), _ptr(parents), _ptr(draft_row),
                                         _ptr(uniforms), rule, B, n, V, depth, _ptr(accepted_len), _ptr(path),
@@ -507,18 +582,23 @@ def accept_into(target_logits, tokens, parents, draft_row, depth, uniforms, draf
 
 
 def accept(target_logits, tokens, parents, draft_row, depth: int, uniforms=None, draft_logits=None,
-           draft_lse=None, without_replacement: bool = False):
+           draft_lse=None, without_replacement: bool = False, sampling: Optional[Sampling] = None):
     """-> (accepted_len [B] int32, path [B][depth] int32, bonus [B] int32).  without_replacement: after a
-    sampled child is rejected its token leaves the draft distribution (q renormalised)."""
+    sampled child is rejected its token leaves the draft distribution (q renormalised).  sampling: the target
+    distribution under each sequence's temperature, top-k, top-p and min-p (sampled acceptance only)."""
     _need_cuda(target_logits, tokens, parents, draft_row, uniforms, draft_logits, draft_lse)
     B, n1, V = target_logits.shape
+    if sampling is not None:
+        if uniforms is None:
+            raise EagleError("accept: sampling parameters need uniforms")
+        sampling.check(B, target_logits)
     dev = target_logits.device
     acc = torch.empty(B, dtype=torch.int32, device=dev)
     path = torch.empty(B, depth, dtype=torch.int32, device=dev)
     bonus = torch.empty(B, dtype=torch.int32, device=dev)
     ws = _workspace(accept_workspace_bytes(B, n1 - 1, V, _dtype_code(target_logits)), dev)
     accept_into(target_logits, tokens, parents, draft_row, depth, uniforms, draft_logits, draft_lse,
-                acc, path, bonus, ws, without_replacement)
+                acc, path, bonus, ws, without_replacement, sampling)
     return acc, path, bonus
 
 
@@ -540,23 +620,28 @@ def step_in(draft_logits, target_logits, depth, k, m, q, k_cache, v_cache, prefi
                   SAMPLE_WITHOUT_REPLACEMENT if without_replacement else SAMPLE_WITH_REPLACEMENT, *paged)
 
 
-def step_workspace_bytes(si: StepIn) -> int:
-    return lib().eagle_verify_step_workspace_bytes(ctypes.byref(si))
+def step_options(sinks: int = 0, sampling: Optional[Sampling] = None) -> StepOptions:
+    """The C step's options: a window's sinks and the sequences' sampling parameters."""
+    return StepOptions(sinks, None if sampling is None else ctypes.pointer(sampling.struct()))
+
+
+def step_workspace_bytes(si: StepIn, options: Optional[StepOptions] = None) -> int:
+    return lib().eagle_verify_step_options_workspace_bytes(ctypes.byref(si), options)
 
 
 def step_into(si: StepIn, tree: Tree, mask, pos, attn_out, accepted_len, path, bonus, ws: torch.Tensor,
-              device) -> int:
+              device, options: Optional[StepOptions] = None) -> int:
     """Enqueue one whole step (build + fused mask, attention, acceptance) on the current stream."""
     so = StepOut(tree.struct(), _ptr(mask), _ptr(pos), _ptr(attn_out), _ptr(accepted_len), _ptr(path), _ptr(bonus))
     n_out = _c_i(0)
-    _check(lib().eagle_verify_step(ctypes.byref(si), ctypes.byref(so), ctypes.byref(n_out), _ptr(ws), ws.numel(),
-                                   _stream(device)), "eagle_verify_step")
+    _check(lib().eagle_verify_step_with_options(ctypes.byref(si), options, ctypes.byref(so), ctypes.byref(n_out),
+                                                _ptr(ws), ws.numel(), _stream(device)), "eagle_verify_step")
     return n_out.value
 
 
-def step_attention_status(si: StepIn, ws: torch.Tensor):
+def step_attention_status(si: StepIn, ws: torch.Tensor, options: Optional[StepOptions] = None):
     """Read the attention's device status word from a step workspace (synchronises)."""
-    off = lib().eagle_verify_step_attention_status_offset(ctypes.byref(si))
+    off = lib().eagle_verify_step_options_attention_status_offset(ctypes.byref(si), options)
     check_attention_status(ws[off:])
 
 

@@ -93,7 +93,9 @@ const char* eagle_status_string(int status) {
 
 const char* eagle_last_cuda_error(void) { return g_cuda_err; }
 
-int eagle_version(void) { return 200; }  // 0.2.0: eagle_step_in_t gained the sampling rule and paged-cache fields
+// 0.2.0: eagle_step_in_t gained the sampling rule and paged-cache fields;
+// 0.3.0: sinks, shared prefixes and sampling parameters (new calls only)
+int eagle_version(void) { return 300; }
 
 // ------------------------------------------------------------------ row stats
 size_t eagle_row_stats_workspace_bytes(long long rows, int V, int dtype, int k) {
@@ -368,6 +370,45 @@ eagle_status eagle_accept_with_rule(const void* target_logits, int target_dtype,
                                    sampling_rule == EAGLE_SAMPLE_WITHOUT_REPLACEMENT));
 }
 
+// ------------------------------------------------- sampling under parameters
+eagle_status eagle_sample(const void* logits, int dtype, long long rows, int V, long long row_stride,
+                          const eagle_sampling_t* params, const float* uniforms, int32_t* tokens, float* logprob,
+                          void* stream) {
+  if (!logits || !uniforms || !tokens) return EAGLE_ERR_NULL;
+  if (!valid_dtype(dtype)) return EAGLE_ERR_DTYPE;
+  if (rows <= 0 || V <= 0 || row_stride < V) return EAGLE_ERR_SHAPE;
+  if (V > kSampleMaxVocab || rows >= (1LL << 27)) return EAGLE_ERR_LIMIT;
+  if ((uintptr_t)logits % dtype_bytes(dtype) != 0) return EAGLE_ERR_ALIGN;
+  const eagle_sampling_t off = {};
+  return cuda_status(launch_sample(logits, dtype, rows, V, row_stride, params ? *params : off, uniforms, tokens, logprob,
+                                   static_cast<cudaStream_t>(stream)));
+}
+
+eagle_status eagle_accept_with_sampling(const void* target_logits, int target_dtype, const void* draft_logits,
+                                        int draft_dtype, const double* draft_lse, int R, const int32_t* tokens,
+                                        const int32_t* parents, const int32_t* draft_row, const float* uniforms,
+                                        int sampling_rule, const eagle_sampling_t* params, int B, int n, int V, int depth,
+                                        int32_t* accepted_len, int32_t* path, int32_t* bonus, void* workspace,
+                                        size_t workspace_bytes, void* stream) {
+  if (!params)
+    return eagle_accept_with_rule(target_logits, target_dtype, draft_logits, draft_dtype, draft_lse, R, tokens, parents,
+                                  draft_row, uniforms, sampling_rule, B, n, V, depth, accepted_len, path, bonus,
+                                  workspace, workspace_bytes, stream);
+  if (sampling_rule != EAGLE_SAMPLE_WITH_REPLACEMENT && sampling_rule != EAGLE_SAMPLE_WITHOUT_REPLACEMENT)
+    return EAGLE_ERR_SHAPE;
+  if (!target_logits || !draft_logits || !draft_lse || !tokens || !parents || !draft_row || !uniforms || !accepted_len ||
+      !path || !bonus)
+    return EAGLE_ERR_NULL;
+  if (!valid_dtype(target_dtype) || draft_dtype != target_dtype) return EAGLE_ERR_DTYPE;
+  if (B <= 0 || n <= 0 || V <= 0 || depth <= 0 || R <= 0) return EAGLE_ERR_SHAPE;
+  if (n > EAGLE_MAX_NODES || depth > EAGLE_MAX_DEPTH || V > kSampleMaxVocab || B >= (1 << 27)) return EAGLE_ERR_LIMIT;
+  if (((uintptr_t)target_logits | (uintptr_t)draft_logits) % dtype_bytes(target_dtype) != 0) return EAGLE_ERR_ALIGN;
+  return cuda_status(launch_accept_sampling(target_logits, target_dtype, draft_logits, draft_lse, R, tokens, parents,
+                                            draft_row, uniforms, *params,
+                                            sampling_rule == EAGLE_SAMPLE_WITHOUT_REPLACEMENT, B, n, V, depth,
+                                            accepted_len, path, bonus, false, static_cast<cudaStream_t>(stream)));
+}
+
 // ------------------------------------------------------ KV-cache compaction
 eagle_status eagle_kv_compact(const void* k_tree, const void* v_tree, const int32_t* path,
                               const int32_t* accepted_len, const int32_t* prefix_len, void* k_cache, void* v_cache,
@@ -421,18 +462,36 @@ bool step_layout(const eagle_step_in_t* in, int sinks, StepLayout* L) {
 extern "C" {
 
 size_t eagle_verify_step_workspace_bytes(const eagle_step_in_t* in) {
-  StepLayout L;
-  return step_layout(in, 0, &L) ? L.total : 0;
+  return eagle_verify_step_options_workspace_bytes(in, nullptr);
 }
 
 size_t eagle_verify_step_attention_status_offset(const eagle_step_in_t* in) {
+  return eagle_verify_step_options_attention_status_offset(in, nullptr);
+}
+
+size_t eagle_verify_step_options_workspace_bytes(const eagle_step_in_t* in, const eagle_step_options_t* options) {
   StepLayout L;
-  return step_layout(in, 0, &L) ? L.attn_off : 0;
+  return step_layout(in, options ? options->sinks : 0, &L) ? L.total : 0;
+}
+
+size_t eagle_verify_step_options_attention_status_offset(const eagle_step_in_t* in, const eagle_step_options_t* options) {
+  StepLayout L;
+  return step_layout(in, options ? options->sinks : 0, &L) ? L.attn_off : 0;
 }
 
 eagle_status eagle_verify_step(const eagle_step_in_t* in, const eagle_step_out_t* out, int* n_nodes,
                                void* workspace, size_t workspace_bytes, void* stream) {
+  return eagle_verify_step_with_options(in, nullptr, out, n_nodes, workspace, workspace_bytes, stream);
+}
+
+eagle_status eagle_verify_step_with_options(const eagle_step_in_t* in, const eagle_step_options_t* options,
+                                            const eagle_step_out_t* out, int* n_nodes, void* workspace,
+                                            size_t workspace_bytes, void* stream) {
   if (!in || !out) return EAGLE_ERR_NULL;
+  const int sinks = options ? options->sinks : 0;
+  const eagle_sampling_t* sampling = options ? options->sampling : nullptr;
+  if (sinks < 0) return EAGLE_ERR_SHAPE;
+  if (sampling && !in->uniforms) return EAGLE_ERR_NULL;
   // --- the checks of the four calls, before anything is launched
   const eagle_tree_t& t = out->tree;
   if (!in->draft_logits || !in->target_logits || !in->q || !in->k_tree || !in->v_tree || !in->prefix_len)
@@ -448,14 +507,16 @@ eagle_status eagle_verify_step(const eagle_step_in_t* in, const eagle_step_out_t
   }
   if (!valid_dtype(in->logits_dtype)) return EAGLE_ERR_DTYPE;
   if (in->B <= 0 || in->V <= 0 || in->depth <= 0 || in->k <= 0 || in->m <= 0) return EAGLE_ERR_SHAPE;
+  if (((uintptr_t)in->target_logits | (uintptr_t)in->draft_logits) % dtype_bytes(in->logits_dtype) != 0 && sampling)
+    return EAGLE_ERR_ALIGN;
   if (in->Hq <= 0 || in->Hkv <= 0 || in->Lmax < 0 || in->window < 0 || in->Hq % in->Hkv != 0) return EAGLE_ERR_SHAPE;
   if (in->depth > EAGLE_MAX_DEPTH || in->k > EAGLE_MAX_TOPK || in->k > in->V || in->m > EAGLE_MAX_NODES)
     return EAGLE_ERR_LIMIT;
   if (in->D != 64 && in->D != 128) return EAGLE_ERR_LIMIT;
   StepLayout L;
-  if (!step_layout(in, 0, &L)) return EAGLE_ERR_LIMIT;
+  if (!step_layout(in, sinks, &L)) return EAGLE_ERR_LIMIT;
   if ((long long)in->B * (L.n + 1) > 0x7fffffffLL) return EAGLE_ERR_SHAPE;
-  if (in->uniforms && in->V > accept_max_vocab(in->logits_dtype)) return EAGLE_ERR_LIMIT;
+  if (in->uniforms && in->V > (sampling ? kSampleMaxVocab : accept_max_vocab(in->logits_dtype))) return EAGLE_ERR_LIMIT;
   if (in->sampling_rule != EAGLE_SAMPLE_WITH_REPLACEMENT && in->sampling_rule != EAGLE_SAMPLE_WITHOUT_REPLACEMENT)
     return EAGLE_ERR_SHAPE;
   if (!aligned16(in->q) || !aligned16(in->k_tree) || !aligned16(in->v_tree) || !aligned16(out->attn_out) ||
@@ -490,8 +551,14 @@ eagle_status eagle_verify_step(const eagle_step_in_t* in, const eagle_step_out_t
                  in->B, n, in->Hq, in->Hkv, in->D, in->window, scale, out->attn_out, ws + L.attn_off};
   at.pg = paged ? &pg : nullptr;
   at.early = true;
+  at.sinks = sinks;
   e = launch_tree_attention(at, s);
   if (e != cudaSuccess) return cuda_status(e);
+  if (sampling)
+    return cuda_status(launch_accept_sampling(in->target_logits, in->logits_dtype, in->draft_logits, t.row_lse, L.R,
+                                              t.tokens, t.parents, t.draft_row, in->uniforms, *sampling,
+                                              in->sampling_rule == EAGLE_SAMPLE_WITHOUT_REPLACEMENT, in->B, n, in->V,
+                                              in->depth, out->accepted_len, out->path, out->bonus, true, s));
   // --- acceptance (the draft rows' log-sum-exps are the tree's row_lse)
   e = launch_accept(in->target_logits, in->logits_dtype, in->draft_logits, in->logits_dtype, t.row_lse, L.R,
                     t.tokens, t.parents, t.draft_row, in->uniforms, in->B, n, in->V, in->depth, out->accepted_len,

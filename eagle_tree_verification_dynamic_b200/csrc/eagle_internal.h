@@ -163,6 +163,17 @@ cudaError_t launch_kv_compact(const void* k_tree, const void* v_tree, const int3
                               const int32_t* prefix_len, void* k_cache, void* v_cache, int32_t* new_len, int B, int n,
                               int Hkv, int D, int Lmax, int depth, cudaStream_t s, const PagedKV* pg = nullptr);
 
+// ---- sampling and acceptance under sampling parameters (sample.cu)
+constexpr int kSampleMaxVocab = 262144;
+cudaError_t launch_sample(const void* logits, int dtype, long long rows, int V, long long stride,
+                          const eagle_sampling_t& params, const float* uniforms, int32_t* tokens, float* logprob,
+                          cudaStream_t s);
+cudaError_t launch_accept_sampling(const void* tgt, int dtype, const void* dft, const double* dlse, int R,
+                                   const int32_t* tokens, const int32_t* parents, const int32_t* draft_row,
+                                   const float* uniforms, const eagle_sampling_t& params, bool without_replacement, int B,
+                                   int n, int V, int depth, int32_t* accepted_len, int32_t* path, int32_t* bonus,
+                                   bool pdl, cudaStream_t s);
+
 // ---- accept (accept.cu)
 size_t accept_ws_bytes(int B, int n, int V, int dtype);
 int accept_max_vocab(int dtype);  // largest V the sampled walk supports

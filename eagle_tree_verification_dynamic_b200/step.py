@@ -34,6 +34,7 @@ class StepShape:
     stochastic: bool = True
     without_replacement: bool = False   # sampled acceptance: a rejected child's token leaves q
     paged: bool = False                 # prefix cache as page pools + block table (Lmax = pages_per_seq x page_size)
+    sinks: int = 0                      # first keys that stay visible under the window
 
     @property
     def R(self) -> int:
@@ -60,11 +61,12 @@ class VerifyStep:
         self.path = torch.empty(s.B, s.depth, dtype=torch.int32, device=dev)
         self.bonus = torch.empty(s.B, dtype=torch.int32, device=dev)
         self.ws_build = L._workspace(L.tree_build_workspace_bytes(s.B, s.R, s.V, dcode, s.k), dev)
-        self.ws_attn = L._workspace(L.attention_workspace_bytes(s.B, n, s.Hq, s.Hkv, s.D, s.Lmax, s.window), dev)
+        self.ws_attn = L._workspace(L.attention_workspace_bytes(s.B, n, s.Hq, s.Hkv, s.D, s.Lmax, s.window, s.sinks),
+                                    dev)
         self.ws_acc = L._workspace(L.accept_workspace_bytes(s.B, n, s.V, dcode), dev)
         shape_only = L.StepIn(None, None, dcode, s.B, s.V, s.depth, s.k, s.m, None, None, None, None, s.Lmax, None,
                               None, s.Hq, s.Hkv, s.D, s.window, 0.0, None, 0)
-        self.ws_step = L._workspace(L.step_workspace_bytes(shape_only), dev)
+        self.ws_step = L._workspace(L.step_workspace_bytes(shape_only, L.step_options(s.sinks)), dev)
         # the two vocabulary sweeps on their own (for timing them apart from the
         # expansion and the walk): draft rows top-k + lse, target rows argmax + lse
         rows_d, rows_t = s.B * s.R, s.B * (n + 1)
@@ -94,16 +96,17 @@ class VerifyStep:
     def attention(self, q, k_cache, v_cache, prefix_len, k_tree, v_tree, block_table=None):
         if self.s.paged:
             L.tree_attention_paged_into(q, k_cache, v_cache, block_table, prefix_len, k_tree, v_tree, self.mask,
-                                        self.pos, self.out, self.ws_attn, self.s.window)
+                                        self.pos, self.out, self.ws_attn, self.s.window, sinks=self.s.sinks)
         else:
             L.tree_attention_into(q, k_cache, v_cache, prefix_len, k_tree, v_tree, self.mask, self.pos, self.out,
-                                  self.ws_attn, self.s.window)
+                                  self.ws_attn, self.s.window, sinks=self.s.sinks)
 
-    def accept(self, target_logits, uniforms: Optional[torch.Tensor], draft_logits):
+    def accept(self, target_logits, uniforms: Optional[torch.Tensor], draft_logits,
+               sampling: Optional[L.Sampling] = None):
         if self.s.stochastic:
             L.accept_into(target_logits, self.tree.tokens, self.tree.parents, self.tree.draft_row, self.s.depth,
                           uniforms, draft_logits, self.tree.row_lse, self.accepted_len, self.path, self.bonus,
-                          self.ws_acc, self.s.without_replacement)
+                          self.ws_acc, self.s.without_replacement, sampling)
         else:
             L.accept_into(target_logits, self.tree.tokens, self.tree.parents, self.tree.draft_row, self.s.depth,
                           None, None, None, self.accepted_len, self.path, self.bonus, self.ws_acc)
@@ -116,20 +119,22 @@ class VerifyStep:
                        inp.get("uniforms") if s.stochastic else None, s.window,
                        without_replacement=s.without_replacement,
                        block_table=inp["block_table"] if s.paged else None)
+        options = L.step_options(s.sinks, inp.get("sampling") if s.stochastic else None)
         L.step_into(si, self.tree, self.mask, self.pos, self.out, self.accepted_len, self.path, self.bonus,
-                    self.ws_step, self.device)
-        self._step_in = si
+                    self.ws_step, self.device, options)
+        self._step_in, self._step_options = si, options
         return self.accepted_len, self.path, self.bonus
 
     def fused_attention_status(self):
         """Raise if the last fused step's attention reported a device status."""
-        L.step_attention_status(self._step_in, self.ws_step)
+        L.step_attention_status(self._step_in, self.ws_step, self._step_options)
 
     def __call__(self, inp: dict):
-        """inp: draft_logits, prefix_len, q, k_cache, v_cache, k_tree, v_tree, target_logits, uniforms."""
+        """inp: draft_logits, prefix_len, q, k_cache, v_cache, k_tree, v_tree, target_logits, uniforms; block_table
+        with a paged cache, sampling (Sampling, per sequence) for sampled acceptance under its parameters."""
         self.build(inp["draft_logits"])
         self.mask_(inp["prefix_len"])
         self.attention(inp["q"], inp["k_cache"], inp["v_cache"], inp["prefix_len"], inp["k_tree"], inp["v_tree"],
                        inp.get("block_table"))
-        self.accept(inp["target_logits"], inp.get("uniforms"), inp["draft_logits"])
+        self.accept(inp["target_logits"], inp.get("uniforms"), inp["draft_logits"], inp.get("sampling"))
         return self.accepted_len, self.path, self.bonus

@@ -25,7 +25,9 @@
  * one level at a time for a draft model in the loop (eagle_tree_grow_*), with
  * the EAGLE-4 harness's cost-aware sizing (eagle_cost_at,
  * eagle_size_keep_level); EAGLE-1's static tree (eagle_static_tree_build);
- * sampling without replacement (eagle_accept_with_rule); a paged prefix cache
+ * sampling without replacement (eagle_accept_with_rule); sampling under a
+ * request's temperature, top-k, top-p and min-p, of rows (eagle_sample) and in
+ * the walk (eagle_accept_with_sampling); a paged prefix cache
  * (eagle_tree_attention_paged); a window with sinks (_with_sinks) and a prefix
  * the batch shares (_shared) in the attention; and the accepted path's keys and
  * values into the cache (eagle_kv_compact, _paged).
@@ -343,6 +345,57 @@ EAGLE_API eagle_status eagle_accept(const void* target_logits, int target_dtype,
                           int B, int n, int V, int depth, int32_t* accepted_len, int32_t* path,
                           int32_t* bonus, void* workspace, size_t workspace_bytes, void* stream);
 
+/* -------------------------------------------- sampling under parameters
+ * What a request asks of its samples.  DEVICE arrays, one entry per row (for
+ * the walk: per sequence); a NULL array leaves that parameter off for all.
+ *   temperature  T > 0 (NULL: 1); T <= 0 or NaN: greedy, the argmax alone
+ *   top_k        the k likeliest tokens (ties to the lower id); <= 0 or >= V: off
+ *   top_p        of those, the fewest likeliest ones whose probability among
+ *                them sums to at least top_p (always one); >= 1 or NaN: off
+ *   min_p        of those, the ones at least min_p times as likely as the
+ *                likeliest; <= 0 or NaN: off, above 1 as 1
+ * A row's weights are exp((x - max) / T) as multiples of 2^-44: a token below
+ * 2^-45 of the likeliest is never drawn.  Logits may be -inf (or NaN, read as
+ * -inf): masked tokens, never drawn; where some are +inf, those alone are left,
+ * equally likely. */
+typedef struct {
+  const float* temperature;
+  const int32_t* top_k;
+  const float* top_p;
+  const float* min_p;
+} eagle_sampling_t;
+
+/* eagle_sample: a token per row from given random numbers.
+ *   logits   [rows] rows of V (dtype), row i at logits + i * row_stride elements
+ *            (row_stride >= V; rows need only their element's alignment)
+ *   params   HOST struct, or NULL (plain softmax sampling)
+ *   uniforms [rows] float in [0, 1), read as eagle_accept reads u_res
+ *   tokens   [rows] int32: the smallest kept id whose cumulative kept weight, in
+ *            id order, exceeds uniforms[i] times the row's kept total; -1 for a
+ *            row that holds only -inf and NaN
+ *   logprob  [rows] float or NULL: log of that token's probability among the
+ *            kept ones (-inf for a row without a token)
+ * One launch, no workspace.  Limits: V <= 262144, rows <= 2^27 - 1. */
+EAGLE_API eagle_status eagle_sample(const void* logits, int dtype, long long rows, int V, long long row_stride,
+                                    const eagle_sampling_t* params, const float* uniforms, int32_t* tokens,
+                                    float* logprob, void* stream);
+
+/* eagle_accept_with_sampling: the sampled walk of eagle_accept_with_rule where
+ * p is the target distribution under the sequence's parameters (params: HOST
+ * struct of [B] arrays; NULL is eagle_accept_with_rule), normalised over what
+ * they keep; q stays the draft row's softmax.  A drafted token that the
+ * parameters remove is rejected, and the bonus is drawn from what they keep.
+ * A target row of -inf and NaN accepts nothing and gives bonus -1.  Only the
+ * target rows that the walk visits are read.  uniforms [B][2][n+1] is required;
+ * limits V <= 262144; the workspace is eagle_accept's (unused with params). */
+EAGLE_API eagle_status eagle_accept_with_sampling(const void* target_logits, int target_dtype,
+                                                  const void* draft_logits, int draft_dtype, const double* draft_lse,
+                                                  int R, const int32_t* tokens, const int32_t* parents,
+                                                  const int32_t* draft_row, const float* uniforms, int sampling_rule,
+                                                  const eagle_sampling_t* params, int B, int n, int V, int depth,
+                                                  int32_t* accepted_len, int32_t* path, int32_t* bonus,
+                                                  void* workspace, size_t workspace_bytes, void* stream);
+
 /* ------------------------------------------- tree grown one level at a time
  * The build of eagle_tree_build for a draft model that produces each level's
  * distributions only once it knows the frontier ("EAGLE" notes, EAGLE-2
@@ -577,6 +630,22 @@ EAGLE_API size_t eagle_verify_step_workspace_bytes(const eagle_step_in_t* in);
 EAGLE_API size_t eagle_verify_step_attention_status_offset(const eagle_step_in_t* in);
 EAGLE_API eagle_status eagle_verify_step(const eagle_step_in_t* in, const eagle_step_out_t* out, int* n_nodes,
                                          void* workspace, size_t workspace_bytes, void* stream);
+
+/* The step with a window's sinks (eagle_tree_attention_with_sinks) and the
+ * requests' sampling parameters (eagle_accept_with_sampling; needs
+ * in->uniforms).  options: HOST struct; NULL, or zeros, is eagle_verify_step.
+ * Its workspace and status offset come from the functions beside it. */
+typedef struct {
+  int sinks;
+  const eagle_sampling_t* sampling; /* HOST struct of [B] device arrays, or NULL */
+} eagle_step_options_t;
+EAGLE_API size_t eagle_verify_step_options_workspace_bytes(const eagle_step_in_t* in,
+                                                           const eagle_step_options_t* options);
+EAGLE_API size_t eagle_verify_step_options_attention_status_offset(const eagle_step_in_t* in,
+                                                                   const eagle_step_options_t* options);
+EAGLE_API eagle_status eagle_verify_step_with_options(const eagle_step_in_t* in, const eagle_step_options_t* options,
+                                                      const eagle_step_out_t* out, int* n_nodes, void* workspace,
+                                                      size_t workspace_bytes, void* stream);
 
 /* ------------------------------------------------------ diagnostics
  * Not a step of the method: a probe of the attention kernel's failure path.

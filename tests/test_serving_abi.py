@@ -89,3 +89,51 @@ def test_oracle_sinks_are_the_rule_written_out():
                 want = (at >= pos - W + 1 or at < S) and (p < L or bool(anc[i, p - L]))
                 assert vis[i, p] == want, (L, W, S, i, p)
     assert (_visible(20, parents, depth, 0, 4) == _visible(20, parents, depth, 0)).all()
+
+
+def test_sample_validation(lib):
+    def call(**kw):
+        return lib.eagle_sample(kw.get("x", FAKE), kw.get("dt", 0), kw.get("rows", 4), kw.get("V", 100),
+                                kw.get("stride", 100), None, kw.get("u", FAKE), kw.get("tok", FAKE), None, None)
+    assert call(x=None) == 1 and call(u=None) == 1 and call(tok=None) == 1
+    assert call(dt=2) == 3
+    assert call(rows=0) == 2 and call(V=0) == 2 and call(stride=99) == 2
+    assert call(V=262145, stride=262145) == 4 and call(rows=1 << 27) == 4
+    assert call(x=ctypes.c_void_p(0x1002)) == 6 and call(x=ctypes.c_void_p(0x1001), dt=1) == 6
+
+
+def test_accept_with_sampling_validation(lib):
+    prm = et._lib.SamplingStruct()
+
+    def call(**kw):
+        return lib.eagle_accept_with_sampling(
+            kw.get("t", FAKE), kw.get("dt", 0), kw.get("d", FAKE), kw.get("ddt", 0), kw.get("lse", FAKE), kw.get("R", 5),
+            FAKE, FAKE, FAKE, kw.get("u", FAKE), kw.get("rule", 0), ctypes.byref(prm), kw.get("B", 1), kw.get("n", 10),
+            kw.get("V", 1000), kw.get("depth", 3), FAKE, FAKE, FAKE, None, 0, None)
+    assert call(t=None) == 1 and call(d=None) == 1 and call(lse=None) == 1 and call(u=None) == 1
+    assert call(rule=2) == 2 and call(R=0) == 2 and call(B=0) == 2 and call(depth=0) == 2
+    assert call(dt=4) == 3 and call(ddt=1) == 3
+    assert call(n=129) == 4 and call(depth=17) == 4 and call(V=262145) == 4
+    assert call(d=ctypes.c_void_p(0x1002)) == 6
+    # without parameters it is eagle_accept_with_rule, which needs its workspace
+    assert lib.eagle_accept_with_sampling(FAKE, 0, FAKE, 0, FAKE, 5, FAKE, FAKE, FAKE, FAKE, 0, None, 1, 10, 1000, 3, FAKE,
+                                          FAKE, FAKE, None, 0, None) == 5
+
+
+def test_step_options(lib):
+    from eagle_tree_verification_dynamic_b200 import _lib
+    fields = dict(draft_logits=FAKE, target_logits=FAKE, logits_dtype=0, B=1, V=32000, depth=6, k=10, m=60, q=FAKE,
+                  k_cache=FAKE, v_cache=FAKE, prefix_len=FAKE, Lmax=2048, k_tree=FAKE, v_tree=FAKE, Hq=32, Hkv=32, D=128,
+                  window=256, scale=0.0, uniforms=None, sampling_rule=0, block_table=None, page_size=0, pages_per_seq=0,
+                  num_pages=0)
+    step_in = lambda **kw: _lib.StepIn(*[{**fields, **kw}[name] for name, _ in _lib.StepIn._fields_])
+    tree = _lib.TreeStruct(FAKE, FAKE, FAKE, FAKE, None, FAKE, FAKE)
+    out = _lib.StepOut(tree, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE)
+    call = lambda si, opt: lib.eagle_verify_step_with_options(ctypes.byref(si), opt, ctypes.byref(out), None, FAKE, 256, None)
+    assert call(step_in(), None) == 5 and call(step_in(), _lib.step_options(4)) == 5
+    assert call(step_in(), _lib.step_options(-1)) == 2
+    assert call(step_in(), _lib.step_options(0, et.Sampling())) == 1           # sampling without uniforms
+    assert call(step_in(uniforms=FAKE), _lib.step_options(0, et.Sampling())) == 5
+    plain = lib.eagle_verify_step_workspace_bytes(ctypes.byref(step_in()))
+    assert lib.eagle_verify_step_options_workspace_bytes(ctypes.byref(step_in()), None) == plain
+    assert lib.eagle_verify_step_options_workspace_bytes(ctypes.byref(step_in()), _lib.step_options(64)) >= plain
