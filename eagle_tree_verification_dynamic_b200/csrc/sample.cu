@@ -16,9 +16,20 @@
 // cumulative sums of any split of the row and a second pass over part of it all
 // agree, and a draw cannot fall between two partial sums.
 //
-// One thread-block cluster holds a row in its shared memory (each logit is read
-// from memory once) and passes over it there; a CTA has a contiguous slice, its
-// threads take the slice's 16-byte vectors in turn.
+// One thread-block cluster takes a row, each CTA a contiguous slice.  The row is
+// read once in full, into counts by value: a bin per pattern of a logit's upper
+// 16 bits (sign, exponent, 7 mantissa bits), kept in shared memory and summed
+// over the cluster.
+//   bf16  a bin is one value, so the counts hold all there is to know: weights are
+//         evaluated once per bin, the cuts of top-k and top-p fall out of prefix
+//         sums over the bins, and each CTA's share of S out of its own counts.
+//         Only the CTA that the draw falls into reads its slice again.
+//   fp32  the bins tell where a cut lies; the few tokens in the bins around it are
+//         gathered into a list, sorted and cut exactly, in a second pass that also
+//         adds up the exact weights (fp64 exponentials) of the tokens above them.
+// What the bins cannot place (logits of 512 and more, a list that overflows, an
+// estimate that missed) is cut by halving the ordered bit patterns of the logits,
+// one pass over the slices per step.
 #include <cooperative_groups.h>
 
 #include <map>
@@ -31,44 +42,97 @@ namespace cg = cooperative_groups;
 
 namespace eagle {
 
+typedef unsigned long long u64;
+
 constexpr int kSmpThreads = 256;
 constexpr int kSmpWarps = kSmpThreads / 32;
 constexpr int kSmpMaxCluster = 16;
-constexpr int kSmpSliceBytes = 32 * 1024;     // of a row per CTA, up to kSmpMaxCluster CTAs
-constexpr int kSmpMaxSliceBytes = 64 * 1024;  // the most a CTA holds (the widest fp32 rows)
-constexpr int kSmpMaxRounds = kSmpMaxSliceBytes / 16 / kSmpThreads + 1;
+constexpr int kSmpBatch = 4;  // 16-byte loads a thread has in flight
 constexpr int kWeightBits = 44;
+constexpr int kListCap = 1024;  // fp32: tokens gathered around a cut
+
+// Bins in descending order of value: 0 = 512 and above (and NaN), then the
+// positive patterns down to 2^-16, one bin for everything smaller in magnitude
+// (kZeroBin, read as 0), the negative patterns down, and last = -512 and below.
+constexpr int kPatLow = (127 - 16) << 7, kPatHigh = (127 + 9) << 7;
+constexpr int kZeroBin = kPatHigh - kPatLow + 1;
+constexpr int kLastBin = 2 * kZeroBin;
+constexpr int kBins = kLastBin + 1;
+constexpr int kBinWords = (kBins + 3) / 4 * 4;
 
 struct SmpShared {
-  double tab[32];                                 // 2^(44 - j/32)
-  unsigned long long xch[2][2][kSmpMaxCluster];  // [parity][value][rank]: what the CTAs tell one another
-  unsigned long long warp_part[2][kSmpWarps];
-  unsigned long long round_part[kSmpMaxRounds * kSmpWarps];
-  unsigned long long pick_base;
-  int pick_entry;
-  int cut_id;
+  double tab[32];                   // 2^(44 - j/32)
+  u64 xch[2][2][kSmpMaxCluster];    // [parity][value][rank]: what the CTAs tell one another
+  u64 word[2][2];                   // [parity]: what one CTA tells all
+  u64 warp_part[2][kSmpWarps];
+  u64 cta_mass[kSmpMaxCluster];     // kept weight of each CTA's slice
+  u64 list[kListCap];               // CTA 0: (order bits, ~id) of the tokens gathered
+  u64 pick_base;
+  int pick_entry, pick_id;
+  int list_n;
+  unsigned n_tiny;
 };
 
-// A CTA's slice of a row: vectors of 16 bytes in shared memory; what lies
-// outside the row is -inf.  Element e of vector v is token first + v * kPerVec + e.
+// A CTA's slice of a row in global memory: vectors of 16 bytes; element e of
+// vector v is token first + v * kPerVec + e; what lies outside the row reads as -inf.
 template <typename T>
 struct RowSlice {
-  uint4* vec;
-  int nvec;
-  int first;
+  const T* row;
+  int V, first, nvec;
+  __device__ __forceinline__ uint4 get(int v) const {
+    constexpr int E = Elem<T>::kPerVec;
+    const int id = first + v * E;
+    if (id >= 0 && id + E <= V) return __ldg(reinterpret_cast<const uint4*>(row + id));
+    const uint4 none = Elem<T>::neg_inf_vec();
+    uint32_t w[4] = {none.x, none.y, none.z, none.w};
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      if (id + e >= 0 && id + e < V) {
+        if (sizeof(T) == 4) {
+          w[e] = __ldg(reinterpret_cast<const unsigned*>(row) + id + e);
+        } else {
+          const uint32_t h = __ldg(reinterpret_cast<const unsigned short*>(row) + id + e);
+          w[e / 2] = (e & 1) ? (w[e / 2] & 0xffffu) | (h << 16) : (w[e / 2] & 0xffff0000u) | h;
+        }
+      }
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
 };
+
+// A CTA's part of the row at `row` (element aligned; it may start inside a vector,
+// so that the vectors inside it are aligned).
+template <typename T>
+__device__ __forceinline__ void place_slice(RowSlice<T>& sl, const T* row, int V, int per, int rank) {
+  constexpr int E = Elem<T>::kPerVec;
+  const int off = (int)(((uintptr_t)row & 15u) / sizeof(T));
+  sl.row = row;
+  sl.V = V;
+  sl.first = rank * per * E - off;
+  sl.nvec = max(0, min(per, (V + off + E - 1) / E - rank * per));
+}
 
 // Per-row constants.
 struct RowStat {
   float top;       // M
-  bool infinite;   // the row held +inf: those tokens count as 0, all others as -inf
+  bool infinite;   // the row holds +inf: those tokens count as 0, all others as -inf
+  bool merged;     // bf16: values below 2^-16 in magnitude are read as 0, as the bins do
   double c32;      // 32 log2(e) / T
   float c;         // log2(e) / T, for skipping weights that round to 0
   float vcut;      // kept: x > vcut, or x == vcut and id <= idcut, and x >= floor
   int idcut;
   float floor;
-  unsigned long long total;  // S (0: nothing to draw)
+  u64 total;       // S (0: nothing to draw)
 };
+
+// A logit as the passes over the row read it, see RowStat::infinite and merged
+// (filter_row makes sure that no sum notices the latter).
+template <typename T>
+__device__ __forceinline__ float canon(const RowStat& s, float x) {
+  if (s.infinite) return x == INFINITY ? 0.f : -INFINITY;
+  if (sizeof(T) == 2 && s.merged) return fabsf(x) < 0x1p-16f ? 0.f : x;
+  return x;
+}
 
 __device__ __forceinline__ bool kept(const RowStat& s, float x, int id) {
   return (x > s.vcut || (x == s.vcut && id <= s.idcut)) && x >= s.floor;
@@ -80,7 +144,7 @@ __device__ __forceinline__ bool kept(const RowStat& s, float x, int id) {
 // term is below 6e-10 relative), all in fp64: an fp32 weight (error 2^-24) would
 // move the cumulative sums of a wide row by more than a small weight's width and
 // with it the token.
-__device__ __forceinline__ unsigned long long weight(const RowStat& s, const double* tab, float x) {
+__device__ __forceinline__ u64 weight(const RowStat& s, const double* tab, float x) {
   if (!((s.top - x) * s.c < 45.5f)) return 0ull;  // also NaN and -inf
   constexpr double kMagic = 6755399441055744.0;   // 1.5 * 2^52: adding it rounds to an integer in the low bits
   constexpr double k1 = kLn2 / 32, k2 = k1 * k1 / 2, k3 = k1 * k1 * k1 / 6;
@@ -92,35 +156,90 @@ __device__ __forceinline__ unsigned long long weight(const RowStat& s, const dou
   const double b = tab[n & 31];
   const double e = __hiloint2double(__double2hiint(b) - ((n >> 5) << 20), __double2loint(b));
   const double w = fma(e, p, e) + 4503599627370496.0;  // + 2^52: rounds, integer in the low 52 bits
-  return (unsigned long long)(__double_as_longlong(w) & 0xfffffffffffffll);
+  return (u64)(__double_as_longlong(w) & 0xfffffffffffffll);
 }
 
-__device__ __forceinline__ unsigned long long warp_sum_u64(unsigned long long v) {
+// ------------------------------------------------------------------- bins
+// The bin of a logit with upper half `pat`.
+__device__ __forceinline__ int bin_of(uint32_t pat) {
+  const int t = min(max((int)(pat & 0x7fffu), kPatLow - 1), kPatHigh) - (kPatLow - 1);
+  return (pat & 0x8000u) ? kZeroBin + t : kZeroBin - t;
+}
+// The pattern of a bin (both ends: beyond the range), as the value whose lower
+// half is `low`: for bf16 (low = 0) the bin's one value.
+__device__ __forceinline__ float bin_value(int j, uint32_t low) {
+  const int t = j < kZeroBin ? kZeroBin - j : j - kZeroBin;
+  if (t == 0) return 0.f;
+  return __uint_as_float((j > kZeroBin ? 0x80000000u : 0u) | ((uint32_t)(t + kPatLow - 1) << 16) | low);
+}
+
+// ------------------------------------------------------------------- team
+__device__ __forceinline__ u64 warp_sum_u64(u64 v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
   return v;
 }
+__device__ __forceinline__ u64 warp_scan_u64(u64 v) {  // inclusive
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const u64 y = __shfl_up_sync(kFull, v, o);
+    if ((int)(threadIdx.x & 31) >= o) v += y;
+  }
+  return v;
+}
+
+// Another CTA's shared memory: one word per access, in the cluster's window.
+__device__ __forceinline__ uint32_t remote(const void* p, int rank) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
+               : "=r"(a) : "r"((uint32_t)__cvta_generic_to_shared(p)), "r"(rank));
+  return a;
+}
+__device__ __forceinline__ void remote_store(uint32_t a, u64 v) {
+  asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(a), "l"(v) : "memory");
+}
+__device__ __forceinline__ u64 remote_load(uint32_t a) {
+  u64 v;
+  asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t remote_load32(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ int remote_add(uint32_t a, int v) {
+  int o;
+  asm volatile("atom.shared::cluster.add.s32 %0, [%1], %2;" : "=r"(o) : "r"(a), "r"(v) : "memory");
+  return o;
+}
+// Cluster barrier for warps whose lanes may arrive at different times (a pass
+// over a ragged slice comes right before it): the warp is brought together first
+// and the barrier is the form without .aligned.
+__device__ __forceinline__ void cluster_sync() {
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+  __syncwarp();
+}
+// (end of the remote accesses)
 
 // The cluster as seen by the passes over one row.
 struct Team {
   cg::cluster_group cl;
   SmpShared* sm;
+  uint32_t* bins;  // this CTA's counts [kBinWords]
+  uint32_t* sums;  // the cluster's counts of this CTA's segment of the bins
   int rank, size, parity;
 
   // Two numbers per CTA (each thread's a and b summed over the CTA, or their
-  // maxima) told to every CTA: xch[.][0 / 1][rank] after it.  Buffers alternate:
-  // a CTA writes a buffer again only after the call between, whose barrier every
-  // CTA reached after its last read.
+  // maxima) told to every CTA: result[0 / 1][rank].  Buffers alternate: a CTA
+  // writes a buffer again only after the call between, whose barrier every CTA
+  // reached after its last read.
   template <bool MAX>
-  __device__ __forceinline__ const unsigned long long (*tell(unsigned long long a, unsigned long long b))[kSmpMaxCluster] {
+  __device__ __forceinline__ const u64 (*tell(u64 a, u64 b))[kSmpMaxCluster] {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    if (MAX) {
-      a = warp_max_u64(a);
-      b = warp_max_u64(b);
-    } else {
-      a = warp_sum_u64(a);
-      b = warp_sum_u64(b);
-    }
+    a = MAX ? warp_max_u64(a) : warp_sum_u64(a);
+    b = MAX ? warp_max_u64(b) : warp_sum_u64(b);
     if (lane == 0) {
       sm->warp_part[0][warp] = a;
       sm->warp_part[1][warp] = b;
@@ -129,17 +248,17 @@ struct Team {
     parity ^= 1;
     if ((int)threadIdx.x < 2 * size) {
       const int which = threadIdx.x & 1, to = threadIdx.x >> 1;
-      unsigned long long v = 0;
+      u64 v = 0;
       for (int w = 0; w < kSmpWarps; ++w) {
-        const unsigned long long y = sm->warp_part[which][w];
+        const u64 y = sm->warp_part[which][w];
         v = MAX ? umax64(v, y) : v + y;
       }
-      *cl.map_shared_rank(&sm->xch[parity][which][rank], to) = v;
+      remote_store(remote(&sm->xch[parity][which][rank], to), v);
     }
-    cl.sync();
+    cluster_sync();
     return sm->xch[parity];
   }
-  __device__ __forceinline__ void sums(unsigned long long& a, unsigned long long& b) {
+  __device__ __forceinline__ void sums2(u64& a, u64& b) {
     const auto x = tell<false>(a, b);
     a = b = 0;
     for (int r = 0; r < size; ++r) {
@@ -147,140 +266,130 @@ struct Team {
       b += x[1][r];
     }
   }
-  __device__ __forceinline__ unsigned long long max1(unsigned long long a) {
-    const auto x = tell<true>(a, 0);
-    a = 0;
-    for (int r = 0; r < size; ++r) a = umax64(a, x[0][r]);
-    return a;
+  // The calling thread (one of the cluster) writes two words to every CTA; all
+  // then call heard(), which returns them.
+  __device__ __forceinline__ void say(u64 a, u64 b) {
+    for (int r = 0; r < size; ++r) {
+      remote_store(remote(&sm->word[parity ^ 1][0], r), a);
+      remote_store(remote(&sm->word[parity ^ 1][1], r), b);
+    }
+  }
+  __device__ __forceinline__ const u64* heard() {
+    parity ^= 1;
+    cluster_sync();
+    return sm->word[parity];
   }
 };
 
 template <typename T, typename F>
 __device__ __forceinline__ void each(const RowSlice<T>& sl, F&& f) {
   constexpr int E = Elem<T>::kPerVec;
-  for (int v = threadIdx.x; v < sl.nvec; v += kSmpThreads) {
-    float x[E];
-    Elem<T>::unpack(sl.vec[v], x);
-    const int id = sl.first + v * E;
+  for (int v0 = threadIdx.x; v0 < sl.nvec; v0 += kSmpThreads * kSmpBatch) {
+    uint4 u[kSmpBatch];
 #pragma unroll
-    for (int e = 0; e < E; ++e) f(x[e], id + e);
+    for (int i = 0; i < kSmpBatch; ++i) {
+      const int v = v0 + i * kSmpThreads;
+      u[i] = v < sl.nvec ? sl.get(v) : Elem<T>::neg_inf_vec();
+    }
+#pragma unroll
+    for (int i = 0; i < kSmpBatch; ++i) {
+      const int v = v0 + i * kSmpThreads;
+      if (v >= sl.nvec) break;
+      float x[E];
+      Elem<T>::unpack(u[i], x);
+      const int id = sl.first + v * E;
+#pragma unroll
+      for (int e = 0; e < E; ++e) f(x[e], id + e);
+    }
   }
 }
 
-// The smallest id whose cumulative g(x, id) (a non-negative integer) exceeds
-// thr, in the CTA that holds it: the thread with that token calls hit(id, x).
-// thr < the total over the row.
+// All threads of one CTA: the smallest id of its slice whose cumulative g(x, id)
+// (a non-negative integer) exceeds thr, thr < the slice's total: the thread with
+// that token calls hit(id, x).
 template <typename T, typename G, typename H>
-__device__ __forceinline__ void select(Team& tm, const RowSlice<T>& sl, unsigned long long thr, G&& g, H&& hit) {
+__device__ __forceinline__ void select_local(SmpShared& sm, const RowSlice<T>& sl, u64 thr, G&& g, H&& hit) {
   constexpr int E = Elem<T>::kPerVec;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  SmpShared& sm = *tm.sm;
-  unsigned long long mine = 0;
-  each<T>(sl, [&](float x, int id) { mine += g(x, id); });
-  const auto x = tm.tell<false>(mine, 0);
-  unsigned long long before = 0;
-  int owner = -1;
-  for (int r = 0; r < tm.size; ++r) {
-    const unsigned long long c = x[0][r];
-    if (owner < 0 && thr < before + c) owner = r;
-    if (owner < 0) before += c;
-  }
-  if (owner != tm.rank) return;  // the same in every thread of the CTA
-  // rounds of 256 vectors in id order, a warp's 32 at a time
-  const int rounds = (sl.nvec + kSmpThreads - 1) / kSmpThreads;
-  auto lane_sum = [&](int v) {
-    unsigned long long s = 0;
-    if (v < sl.nvec) {
-      float y[E];
-      Elem<T>::unpack(sl.vec[v], y);
+  auto vec_sum = [&](const uint4& u, int v) {
+    float y[E];
+    Elem<T>::unpack(u, y);
+    u64 s = 0;
 #pragma unroll
-      for (int e = 0; e < E; ++e) s += g(y[e], sl.first + v * E + e);
-    }
+    for (int e = 0; e < E; ++e) s += g(y[e], sl.first + v * E + e);
     return s;
   };
-  for (int q = 0; q < rounds; ++q) {
-    const unsigned long long s = warp_sum_u64(lane_sum(q * kSmpThreads + tid));
-    if (lane == 0) sm.round_part[q * kSmpWarps + warp] = s;
-  }
-  __syncthreads();
-  if (warp == 0) {
-    unsigned long long base = before;
-    for (int e0 = 0; e0 < rounds * kSmpWarps; e0 += 32) {
-      const unsigned long long c = e0 + lane < rounds * kSmpWarps ? sm.round_part[e0 + lane] : 0;
-      unsigned long long inc = c;
+  // ids ascend with the round (256 vectors), the warp and the lane: find the
+  // round and warp first
+  u64 base = 0;
+  const int rounds = (sl.nvec + kSmpThreads - 1) / kSmpThreads;
+  int entry = -1;
+  for (int q0 = 0; q0 < rounds; q0 += kSmpBatch) {
+    uint4 u[kSmpBatch];
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const unsigned long long y = __shfl_up_sync(kFull, inc, o);
-        if (lane >= o) inc += y;
-      }
-      const unsigned m = __ballot_sync(kFull, thr < base + inc);
-      if (m) {
-        if (lane == __ffs(m) - 1) {
-          sm.pick_entry = e0 + lane;
-          sm.pick_base = base + inc - c;
-        }
-        break;
-      }
-      base += __shfl_sync(kFull, inc, 31);
+    for (int i = 0; i < kSmpBatch; ++i) {
+      const int v = (q0 + i) * kSmpThreads + tid;
+      u[i] = v < sl.nvec ? sl.get(v) : Elem<T>::neg_inf_vec();
     }
-  }
-  __syncthreads();
-  if (sm.pick_entry % kSmpWarps != warp) return;
-  const int v = sm.pick_entry / kSmpWarps * kSmpThreads + tid;
-  const unsigned long long c = lane_sum(v);
-  unsigned long long inc = c;
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const unsigned long long y = __shfl_up_sync(kFull, inc, o);
-    if (lane >= o) inc += y;
+    for (int i = 0; i < kSmpBatch; ++i) {
+      const int v = (q0 + i) * kSmpThreads + tid;
+      const u64 s = warp_sum_u64(v < sl.nvec ? vec_sum(u[i], v) : 0);
+      if (lane == 0) sm.list[i * kSmpWarps + warp] = s;
+    }
+    __syncthreads();
+    const u64 c = sm.list[lane];  // kSmpBatch * kSmpWarps = 32 entries, in id order
+    static_assert(kSmpBatch * kSmpWarps == 32, "one entry per lane");
+    const u64 inc = warp_scan_u64(c);
+    const unsigned m = __ballot_sync(kFull, thr < base + inc);
+    if (m) {
+      const int src = __ffs(m) - 1;
+      entry = q0 * kSmpWarps + src;
+      base += __shfl_sync(kFull, inc - c, src);
+      break;
+    }
+    base += __shfl_sync(kFull, inc, 31);
+    __syncthreads();
   }
-  unsigned long long cum = sm.pick_base + inc - c;
+  if (entry < 0 || entry % kSmpWarps != warp) return;
+  const int v = entry / kSmpWarps * kSmpThreads + tid;
+  const uint4 u = v < sl.nvec ? sl.get(v) : Elem<T>::neg_inf_vec();
+  const u64 c = v < sl.nvec ? vec_sum(u, v) : 0;
+  u64 cum = base + warp_scan_u64(c) - c;
   if (thr < cum || thr >= cum + c) return;
   float y[E];
-  Elem<T>::unpack(sl.vec[v], y);
-  const int id = sl.first + v * E;
+  Elem<T>::unpack(u, y);
   bool done = false;
 #pragma unroll
   for (int e = 0; e < E; ++e) {
-    cum += g(y[e], id + e);
+    cum += g(y[e], sl.first + v * E + e);
     if (!done && thr < cum) {
       done = true;
-      hit(id + e, y[e]);
+      hit(sl.first + v * E + e, y[e]);
     }
   }
 }
 
-// A CTA's part of a row at `row` (element aligned), and filling it: 16-byte copies
-// where the row covers the whole vector, single elements at its two ends.
-template <typename T>
-__device__ __forceinline__ void place_slice(RowSlice<T>& sl, const T* row, int V, int per, int rank) {
-  constexpr int E = Elem<T>::kPerVec;
-  const int off = (int)(((uintptr_t)row & 15u) / sizeof(T));  // the row starts inside its first vector
-  sl.first = rank * per * E - off;
-  const int all = (V + off + E - 1) / E;
-  sl.nvec = max(0, min(per, all - rank * per));
-}
-template <typename T>
-__device__ __forceinline__ void fill_slice(RowSlice<T>& sl, const T* row, int V) {
-  constexpr int E = Elem<T>::kPerVec;
-  const bool aligned = ((uintptr_t)(row + sl.first) & 15u) == 0;  // else another row's placement, out of step with this one's
-  for (int v = threadIdx.x; v < sl.nvec; v += kSmpThreads) {
-    const int id = sl.first + v * E;
-    if (aligned && id >= 0 && id + E <= V) {
-      const uint32_t dst = (uint32_t)__cvta_generic_to_shared(sl.vec + v);
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(row + id) : "memory");
-    } else {
-      uint4 u = Elem<T>::neg_inf_vec();
-      T* p = reinterpret_cast<T*>(&u);
-      for (int e = 0; e < E; ++e)
-        if (id + e >= 0 && id + e < V) p[e] = row[id + e];
-      sl.vec[v] = u;
-    }
+// The CTA whose part of `x[rank]` holds thr, and what lies before it (size: none).
+__device__ __forceinline__ int owner_of(const u64* x, int size, u64 thr, u64& before) {
+  before = 0;
+  for (int r = 0; r < size; ++r) {
+    if (thr < before + x[r]) return r;
+    before += x[r];
   }
-  asm volatile("cp.async.wait_all;" ::: "memory");
-  // (each thread reads only vectors it copied itself until the next barrier)
+  return size;
 }
 
+// select_local over the cluster: every CTA sums g over its slice first.
+template <typename T, typename G, typename H>
+__device__ __forceinline__ void select(Team& tm, const RowSlice<T>& sl, u64 thr, G&& g, H&& hit) {
+  u64 mine = 0, before;
+  each<T>(sl, [&](float x, int id) { mine += g(x, id); });
+  const auto x = tm.tell<false>(mine, 0);
+  if (owner_of(x[0], tm.size, thr, before) == tm.rank) select_local<T>(*tm.sm, sl, thr - before, g, hit);
+}
+
+// ------------------------------------------------------------ a row's cut
 struct RowParams {
   float temperature, top_p, min_p;
   int top_k;
@@ -295,159 +404,547 @@ __device__ __forceinline__ RowParams row_params(const eagle_sampling_t& s, long 
   return p;
 }
 
-// The row's maximum, cut and total (every thread of every CTA gets the same).
-template <typename T>
-__device__ void filter_row(Team& tm, RowSlice<T>& sl, const RowParams& pr, int V, RowStat& s) {
-  const SmpShared& sm = *tm.sm;
-  {
-    float m = -INFINITY;
-    for (int v = threadIdx.x; v < sl.nvec; v += kSmpThreads) m = fmaxf(m, Elem<T>::vec_max(sl.vec[v]));
-    m = order_value((uint32_t)tm.max1(order_bits(m)));
-    s.infinite = m == INFINITY;
-    if (s.infinite) {  // the likeliest tokens are the infinite ones, alike
-      constexpr int E = Elem<T>::kPerVec;
-      for (int v = threadIdx.x; v < sl.nvec; v += kSmpThreads) {
-        T* p = reinterpret_cast<T*>(sl.vec + v);
-        for (int e = 0; e < E; ++e) p[e] = (float)p[e] == INFINITY ? (T)0.f : (T)-INFINITY;
-      }
-      m = 0.f;
-    }
-    s.top = m;
-  }
-  s.vcut = -INFINITY;
-  s.idcut = 0x7fffffff;
-  s.floor = -INFINITY;
-  s.total = 0;
-  if (s.top == -INFINITY) return;
+// What is asked of a row: k > 0: the first k tokens; by_p: top-p of those.
+struct RowAsk {
+  long long k;
+  bool by_p;
+  float p;
+  float floor;  // min-p as a value: kept tokens are at or above it
+};
+
+__device__ __forceinline__ u64 share_of(float p, u64 Z) {  // ceil(p Z), within [1, Z]
+  const u64 need = (u64)ceil((double)p * (double)Z);
+  return need < 1 ? 1 : (need > Z ? Z : need);
+}
+
+// Row constants once M is known.
+__device__ __forceinline__ RowAsk row_ask(const RowParams& pr, int V, RowStat& s) {
+  RowAsk q;
   const bool greedy = !(pr.temperature > 0.f);
   const double T_ = greedy ? 1.0 : (double)pr.temperature;
   s.c32 = 32.0 * 1.4426950408889634 / T_;
   s.c = (float)fmin(s.c32 / 32.0, 1e30);
-  const bool by_p = !greedy && pr.top_p < 1.f;  // (NaN: off)
-  long long k = greedy || (by_p && !(pr.top_p > 0.f)) ? 1 : (pr.top_k > 0 && pr.top_k < V ? pr.top_k : 0);
+  q.by_p = !greedy && pr.top_p < 1.f;  // (NaN: off)
+  q.p = pr.top_p;
+  q.k = greedy || (q.by_p && !(pr.top_p > 0.f)) ? 1 : (pr.top_k > 0 && pr.top_k < V ? pr.top_k : 0);
+  if (q.k == 1) q.by_p = false;  // one token is its own share
+  q.floor = -INFINITY;
   if (!greedy && pr.min_p > 0.f) {
     // e >= min_p where x >= M + T ln(min_p): the smallest float at or above it
     const double at = pr.min_p >= 1.f ? (double)s.top : (double)s.top + T_ * log((double)pr.min_p);
-    float f = __double2float_ru(at);
-    s.floor = f;
+    q.floor = __double2float_ru(at);
   }
-  auto count_mass = [&](float cut, unsigned long long& n, unsigned long long& m, bool strict, bool mass) {
-    n = m = 0;
-    each<T>(sl, [&](float x, int id) {
-      if (kept(s, x, id) && (strict ? x > cut : x >= cut)) {
-        ++n;
-        if (mass) m += weight(s, sm.tab, x);
-      }
+  return q;
+}
+
+// Cuts by halving the ordered bit patterns, a pass over the row per step; any
+// values, any ties.  Leaves s.vcut, s.idcut and each CTA's kept weight.
+template <typename T>
+__device__ __forceinline__ void cut_by_halving(Team& tm, const RowSlice<T>& sl, const RowParams& pr, int V, RowStat& s) {
+  SmpShared& sm = *tm.sm;
+  s.infinite = s.merged = false;
+  s.total = 0;
+  {
+    float m = -INFINITY;
+    each<T>(sl, [&](float x, int) { m = fmaxf(m, canon<T>(s, x)); });
+    const auto x = tm.tell<true>(order_bits(m), 0);
+    u64 t = 0;
+    for (int r = 0; r < tm.size; ++r) t = umax64(t, x[0][r]);
+    s.top = order_value((uint32_t)t);
+    if (s.top == INFINITY) {
+      s.infinite = true;
+      s.top = 0.f;
+    }
+    if (s.top == -INFINITY) return;  // nothing to draw
+  }
+  s.vcut = s.floor = -INFINITY;
+  s.idcut = 0x7fffffff;
+  const RowAsk ask = row_ask(pr, V, s);
+  auto measure = [&](float cut, bool strict, bool mass) {
+    u64 n = 0, unused = 0;
+    each<T>(sl, [&](float y, int id) {
+      const float x = canon<T>(s, y);
+      if (kept(s, x, id) && (strict ? x > cut : x >= cut)) n += mass ? weight(s, sm.tab, x) : 1ull;
     });
-    tm.sums(n, m);
+    tm.sums2(n, unused);
+    return n;
   };
-  const float floor_ = s.floor;
-  s.floor = -INFINITY;  // min-p comes last: it takes nothing from the sums before it
-  // The largest cut value v with measure(x >= v) >= need, by halving the ordered
-  // bit patterns; then how many of the tokens equal to v belong, by id.
-  auto cut_at = [&](unsigned long long need, bool mass) {
+  // the largest v with measure(x >= v) >= need; then how many of the tokens
+  // equal to v belong, by id
+  auto cut_at = [&](u64 need, bool mass) {
     uint32_t lo = order_bits(-INFINITY) + 1, hi = order_bits(s.top);  // lo always holds enough
-    unsigned long long n, m;
     while (lo < hi) {
       const uint32_t mid = lo + (hi - lo + 1) / 2;
-      count_mass(order_value(mid), n, m, false, mass);
-      if ((mass ? m : n) >= need) lo = mid;
+      if (measure(order_value(mid), false, mass) >= need) lo = mid;
       else hi = mid - 1;
     }
     const float v = order_value(lo);
-    count_mass(v, n, m, true, mass);
-    const unsigned long long one = mass ? weight(s, sm.tab, v) : 1ull;
-    const unsigned long long ties = (need - (mass ? m : n) + one - 1) / one;  // >= 1 of them
-    select<T>(tm, sl, ties - 1, [&](float x, int id) { return (unsigned long long)(x == v && kept(s, x, id)); },
-              [&](int id, float) {
-                for (int r = 0; r < tm.size; ++r) *tm.cl.map_shared_rank(&tm.sm->cut_id, r) = id;
-              });
-    tm.cl.sync();
+    const u64 above = measure(v, true, mass);
+    const u64 one = mass ? weight(s, sm.tab, v) : 1ull;
+    const u64 ties = (need - above + one - 1) / one;  // >= 1 of them
+    select<T>(tm, sl, ties - 1, [&](float y, int id) {
+                const float x = canon<T>(s, y);
+                return (u64)(x == v && kept(s, x, id));
+              }, [&](int id, float) { tm.say((u64)id, 0); });
+    const u64* w = tm.heard();
     s.vcut = v;
-    s.idcut = tm.sm->cut_id;
-    tm.cl.sync();
+    s.idcut = (int)w[0];
   };
-  if (k == 1) {
-    // the first of the largest
-    const float v = s.top;
-    select<T>(tm, sl, 0ull, [&](float x, int) { return (unsigned long long)(x == v); },
-              [&](int id, float) {
-                for (int r = 0; r < tm.size; ++r) *tm.cl.map_shared_rank(&tm.sm->cut_id, r) = id;
-              });
-    tm.cl.sync();
-    s.vcut = v;
-    s.idcut = tm.sm->cut_id;
-    tm.cl.sync();
-  } else if (k > 1) {
-    unsigned long long n, m;
-    count_mass(-INFINITY, n, m, true, false);
-    if (n > (unsigned long long)k) cut_at((unsigned long long)k, false);
-  }
-  if (by_p && k != 1) {
-    unsigned long long n, Z;
-    count_mass(-INFINITY, n, Z, true, true);
-    const unsigned long long need = (unsigned long long)ceil((double)pr.top_p * (double)Z);
-    cut_at(need < 1 ? 1 : (need > Z ? Z : need), true);
-  }
-  s.floor = floor_;
-  unsigned long long S = 0, unused = 0;
-  each<T>(sl, [&](float x, int id) {
-    if (kept(s, x, id)) S += weight(s, sm.tab, x);
+  if (ask.k > 0 && measure(-INFINITY, true, false) > (u64)ask.k) cut_at((u64)ask.k, false);
+  if (ask.by_p) cut_at(share_of(ask.p, measure(-INFINITY, true, true)), true);
+  s.floor = ask.floor;
+  u64 mine = 0;
+  each<T>(sl, [&](float y, int id) {
+    const float x = canon<T>(s, y);
+    if (kept(s, x, id)) mine += weight(s, sm.tab, x);
   });
-  tm.sums(S, unused);
-  s.total = S;
+  const auto x = tm.tell<false>(mine, 0);
+  s.total = 0;
+  for (int r = 0; r < tm.size; ++r) s.total += x[0][r];
+  if (threadIdx.x < tm.size) sm.cta_mass[threadIdx.x] = x[0][threadIdx.x];
+  __syncthreads();
+}
+
+// Sum of `mine` over the threads of the CTA before this one, and over all of them.
+__device__ __forceinline__ u64 cta_exclusive(SmpShared& sm, u64 mine, u64* all) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const u64 own = warp_sum_u64(mine);
+  __syncthreads();
+  if (lane == 0) sm.warp_part[0][warp] = own;
+  __syncthreads();
+  u64 before = 0, total = 0;
+#pragma unroll
+  for (int w = 0; w < kSmpWarps; ++w) {
+    const u64 y = sm.warp_part[0][w];
+    if (w < warp) before += y;
+    total += y;
+  }
+  __syncthreads();
+  if (all) *all = total;
+  return before + warp_scan_u64(mine) - mine;
+}
+
+// The first bin (in descending order of value) at which the running measure of
+// the cluster reaches `need`; per bin `of(j, count)`, per CTA the measure `seg`
+// of its segment, this thread's part `mine` of it (bins [j0, j1)).  Exactly one
+// thread of the cluster calls found(bin, measure before it) if need is reached.
+template <typename O, typename F>
+__device__ __forceinline__ void find_bin(Team& tm, const u64* seg, u64 need, u64 mine, int j0, int j1, int seg0, O&& of,
+                                         F&& found) {
+  u64 before;
+  if (owner_of(seg, tm.size, need - 1, before) != tm.rank) return;
+  u64 at = cta_exclusive(*tm.sm, mine, nullptr) + before;
+  int hit = -1;
+  u64 run = at;
+  if (need > at && need <= at + mine) {
+    for (int j = j0; j < j1 && hit < 0; ++j) {
+      const u64 m = of(j, tm.sums[j - seg0]);
+      if (need <= run + m) hit = j;
+      else run += m;
+    }
+  }
+  if (hit >= 0) found(hit, run);
+}
+
+// Sort n <= kListCap keys of shared memory in descending order (whole CTA).
+__device__ __forceinline__ void sort_list(u64* a, int n) {
+  int size = 1;
+  while (size < n) size <<= 1;
+  for (int i = n + threadIdx.x; i < size; i += kSmpThreads) a[i] = 0;
+  __syncthreads();
+  for (int k = 2; k <= size; k <<= 1) {
+    for (int j = k >> 1; j > 0; j >>= 1) {
+      for (int t = threadIdx.x; t < size / 2; t += kSmpThreads) {
+        const int i = (t / j) * 2 * j + t % j, p = i + j;
+        const u64 x = a[i], y = a[p];
+        const bool desc = (i & k) == 0;
+        if (desc ? x < y : x > y) {
+          a[i] = y;
+          a[p] = x;
+        }
+      }
+      __syncthreads();
+    }
+  }
+}
+
+// The row's maximum, cut, total and each CTA's share of it, by way of the bins;
+// false (in every CTA) for a row that they do not settle.  s.idcut is right for
+// the CTA's own slice (GLOBAL: for every token).
+template <typename T, bool GLOBAL>
+__device__ __forceinline__ bool cut_by_bins(Team& tm, const RowSlice<T>& sl, const RowParams& pr, int V, RowStat& s) {
+  SmpShared& sm = *tm.sm;
+  const int tid = threadIdx.x;
+  constexpr bool kExact = sizeof(T) == 2;  // a bin is one value
+  s.infinite = false;
+  s.merged = kExact;
+  s.vcut = s.floor = -INFINITY;
+  s.idcut = 0x7fffffff;
+  s.total = 0;
+  // ---- counts by value
+  for (int i = tid; i < kBinWords / 4; i += kSmpThreads) reinterpret_cast<uint4*>(tm.bins)[i] = make_uint4(0, 0, 0, 0);
+  if (tid == 0) {
+    sm.list_n = 0;
+    sm.n_tiny = 0;
+  }
+  __syncthreads();
+  float m = -INFINITY;
+  each<T>(sl, [&](float x, int) {
+    atomicAdd(tm.bins + bin_of(__float_as_uint(x) >> 16), 1u);
+    if (!kExact) m = fmaxf(m, x);
+  });
+  // (padding reads as -inf: it only adds to the last bin, which is never used)
+  cluster_sync();
+  // ---- this CTA's segment of the bins, summed over the cluster
+  const int seg = (kBins + tm.size - 1) / tm.size, seg0 = tm.rank * seg, seg1 = min(kBins, seg0 + seg);
+  const int bpt = ((seg + kSmpThreads - 1) / kSmpThreads) | 1;  // odd: threads' bins lie in different banks
+  const int j0 = min(seg1, seg0 + tid * bpt), j1 = min(seg1, j0 + bpt);
+  u64 first = 0;  // order bits of the largest value counted
+  for (int j = j0; j < j1; ++j) {
+    uint32_t c = 0;
+    for (int r = 0; r < tm.size; ++r) c += remote_load32(remote(tm.bins + j, r));
+    tm.sums[j - seg0] = c;
+    if (c && !first && j < kLastBin) first = order_bits(j == 0 ? INFINITY : bin_value(j, 0));
+  }
+  {
+    const auto x = tm.tell<true>(first, kExact ? 0 : order_bits(m));
+    u64 a = 0, b = 0;
+    for (int r = 0; r < tm.size; ++r) {
+      a = umax64(a, x[0][r]);
+      b = umax64(b, x[1][r]);
+    }
+    // nothing but -512 and below, or 512 and above: not for the bins
+    const float lead = a ? order_value((uint32_t)a) : -INFINITY;
+    if (lead == -INFINITY || lead == INFINITY) {
+      return false;
+    }
+    s.top = kExact ? lead : order_value((uint32_t)b);
+  }
+  const RowAsk ask = row_ask(pr, V, s);
+  if (!((s.top + 512.f) * s.c >= 45.5f)) {  // tokens of the last bin would weigh something
+    u64 n = 0, unused = 0;
+    each<T>(sl, [&](float x, int) { n += x <= -512.f && x > -INFINITY; });
+    tm.sums2(n, unused);
+    if (n) {
+      return false;
+    }
+  }
+  // ---- bf16: everything from the counts
+  if constexpr (kExact) {
+    auto mass_of = [&](int j, uint32_t c) { return c && j < kLastBin ? c * weight(s, sm.tab, bin_value(j, 0)) : 0ull; };
+    auto count_of = [&](int j, uint32_t c) { return j < kLastBin ? (u64)c : 0ull; };
+    u64 n = 0, w = 0;
+    for (int j = j0; j < j1; ++j) {
+      const uint32_t c = tm.sums[j - seg0];
+      n += count_of(j, c);
+      if (ask.by_p) w += mass_of(j, c);
+    }
+    u64 ties = ~0ull;  // of the tokens equal to s.vcut
+    int cut_bin = kLastBin;
+    if (ask.k > 0 || ask.by_p) {
+      const auto x = tm.tell<false>(n, w);
+      u64 N = 0, Z = 0;
+      for (int r = 0; r < tm.size; ++r) {
+        N += x[0][r];
+        Z += x[1][r];
+      }
+      if (ask.k > 0 && N > (u64)ask.k) {
+        find_bin(tm, x[0], (u64)ask.k, n, j0, j1, seg0, count_of, [&](int j, u64 at) {
+          // the tokens above the bin, and how many of it
+          tm.say((u64)j, (u64)ask.k - at);
+        });
+        const u64* h = tm.heard();
+        cut_bin = (int)h[0];
+        ties = h[1];
+        if (ask.by_p) {
+          // Z: the weight above the bin, and the ties'
+          u64 above = 0, unused = 0;
+          for (int j = j0; j < min(j1, cut_bin); ++j) above += mass_of(j, tm.sums[j - seg0]);
+          tm.sums2(above, unused);
+          Z = above + ties * weight(s, sm.tab, bin_value(cut_bin, 0));
+        }
+      }
+      if (ask.by_p) {
+        const u64 need = share_of(ask.p, Z);
+        const auto y = tm.tell<false>(n, w);
+        find_bin(tm, y[1], need, w, j0, j1, seg0, mass_of, [&](int j, u64 at) {
+          const u64 one = weight(s, sm.tab, bin_value(j, 0));
+          tm.say((u64)j, (need - at + one - 1) / one);
+        });
+        const u64* h = tm.heard();
+        cut_bin = (int)h[0];
+        ties = h[1];
+      }
+      if (cut_bin < kLastBin) s.vcut = bin_value(cut_bin, 0);
+    }
+    s.floor = ask.floor;
+    // values read as 0 must not show: neither in a sum nor by a cut among them
+    {
+      const u64 zeros = tm.bins[kZeroBin];
+      u64 tiny = 0;
+      if (zeros)
+        each<T>(sl, [&](float x, int) { tiny += x != 0.f && fabsf(x) < 0x1p-16f; });
+      u64 a = 0, mine = 0;
+      // ---- each CTA's kept weight, from its own counts
+      const int from = bin_of(__float_as_uint(s.top) >> 16);
+      for (int j = from + tid; j < cut_bin; j += kSmpThreads) {
+        const uint32_t c = tm.bins[j];
+        if (c == 0) continue;
+        const float v = bin_value(j, 0);
+        if (v < s.floor) break;
+        mine += c * weight(s, sm.tab, v);
+      }
+      a = (tid == 0 && cut_bin < kLastBin ? (u64)tm.bins[cut_bin] : 0ull) + (tiny << 32);
+      const auto x = tm.tell<false>(mine, a);
+      const bool at_floor = cut_bin < kLastBin && s.vcut >= s.floor;  // the tokens equal to the cut are kept
+      const u64 one = at_floor ? weight(s, sm.tab, s.vcut) : 0ull;
+      u64 seen = 0, my_ties = 0, tiny_all = 0;
+      s.total = 0;
+      for (int r = 0; r < tm.size; ++r) {
+        const u64 eq = x[1][r] & 0xffffffffull;
+        const u64 take = ties > seen ? (ties - seen < eq ? ties - seen : eq) : 0;
+        tiny_all += x[1][r] >> 32;
+        if (r == tm.rank) my_ties = take;
+        const u64 mass = x[0][r] + take * one;
+        if (tid == 0) sm.cta_mass[r] = mass;
+        s.total += mass;
+        seen += eq;
+      }
+      __syncthreads();
+      // a value below 2^-16 read as 0 is off by at most 2^-16 c of its weight
+      if (tiny_all &&
+          (cut_bin == kZeroBin || !((double)tiny_all * (double)weight(s, sm.tab, 0.f) * (double)s.c * 0x1p-16 <= (double)s.total * 0x1p-32))) {
+        return false;
+      }
+      if (cut_bin < kLastBin && ties < seen) {
+        // some of the tokens equal to the cut: by id, so all in the CTAs before
+        // one, none in those after it
+        const u64 eq = tm.bins[cut_bin];
+        auto is_tie = [&](float x2, int) { return (u64)(canon<T>(s, x2) == s.vcut); };
+        if constexpr (GLOBAL) {
+          // the CTA that holds the last tie taken finds its id for all
+          u64 before = 0;
+          for (int r = 0; r < tm.rank; ++r) before += x[1][r] & 0xffffffffull;
+          if (ties > before && ties <= before + eq)
+            select_local<T>(sm, sl, ties - before - 1, is_tie, [&](int id, float) { tm.say((u64)id, 0); });
+          s.idcut = (int)tm.heard()[0];
+        } else if (my_ties == 0) {
+          s.idcut = -1;
+        } else if (my_ties < eq) {
+          // (looked up by the CTA that the draw falls into, see sample_kernel)
+          s.idcut = -2 - (int)my_ties;
+        }
+      }
+    }
+    return true;
+  } else {
+    // ---- fp32: exact sums and a list around the cut, in a second pass
+    auto count_of = [&](int j, uint32_t c) { return j < kLastBin ? (u64)c : 0ull; };
+    auto guess_of = [&](int j, uint32_t c) {  // weight of the bin's middle, the bin's at half a percent or so
+      if (!c || j == 0 || j >= kLastBin) return 0ull;
+      const float v = bin_value(j, 0x8000u);
+      return c * weight(s, sm.tab, v < s.top ? v : s.top);
+    };
+    u64 n = 0, w = 0;
+    for (int j = j0; j < j1; ++j) {
+      const uint32_t c = tm.sums[j - seg0];
+      n += count_of(j, c);
+      if (ask.by_p) w += guess_of(j, c);
+    }
+    int lo_bin = 0, hi_bin = -1;  // bins whose tokens are listed
+    bool by_k = false, window = false, slow = false;
+    if (ask.k > 0 || ask.by_p) {
+      const auto x = tm.tell<false>(n, w);
+      u64 N = 0, Zg = 0;
+      for (int r = 0; r < tm.size; ++r) {
+        N += x[0][r];
+        Zg += x[1][r];
+      }
+      by_k = ask.k > 0 && N > (u64)ask.k;
+      window = ask.by_p && !by_k;
+      if (by_k) {
+        find_bin(tm, x[0], (u64)ask.k, n, j0, j1, seg0, count_of,
+                 [&](int j, u64 at) { tm.say((u64)j, at + tm.sums[j - seg0]); });
+        const u64* h = tm.heard();
+        hi_bin = (int)h[0];
+        slow = h[1] > (u64)kListCap;
+      } else if (window) {
+        // the bins where the estimated share may be reached, the estimate taken
+        // to be within 1 part in 64 of what remains on either side
+        const u64 need = share_of(ask.p, Zg), rest = Zg - need;
+        const u64 slack = (need < rest ? need : rest) / 64;
+        const u64 lo = need > slack ? need - slack : 1, hi = need + slack;
+        find_bin(tm, x[1], lo, w, j0, j1, seg0, guess_of, [&](int j, u64) { tm.say((u64)j, 0); });
+        lo_bin = (int)tm.heard()[0];
+        const auto y = tm.tell<false>(n, w);
+        find_bin(tm, y[1], hi, w, j0, j1, seg0, guess_of, [&](int j, u64) { tm.say((u64)j, 0); });
+        hi_bin = (int)tm.heard()[0];
+      }
+    }
+    if (slow) {
+      return false;
+    }
+    const bool listed = hi_bin >= 0;
+    // above: tokens before the listed bins; Z: all
+    u64 Z = 0, above = 0, kept_above = 0;
+    const uint32_t list_n = remote(&sm.list_n, 0), list = remote(sm.list, 0);  // CTA 0's
+    each<T>(sl, [&](float x, int id) {
+      const int j = bin_of(__float_as_uint(x) >> 16);
+      const bool in = listed && j >= lo_bin && j <= hi_bin && x > -INFINITY;
+      const bool before = !listed || j < lo_bin;
+      if ((window || before) && x == x) {
+        const u64 y = weight(s, sm.tab, x);
+        Z += y;
+        if (before) above += y;
+        if (before && x >= ask.floor) kept_above += y;
+      }
+      if (in) {
+        const int at = remote_add(list_n, 1);
+        if (at < kListCap) remote_store(list + 8 * at, make_key(x, id));
+      }
+    });
+    s.floor = ask.floor;
+    if (!listed) {
+      const auto x = tm.tell<false>(kept_above, 0);
+      for (int r = 0; r < tm.size; ++r) {
+        s.total += x[0][r];
+        if (tid == 0) sm.cta_mass[r] = x[0][r];
+      }
+      __syncthreads();
+      return true;
+    }
+    tm.sums2(Z, above);
+    // ---- CTA 0 sorts the list and cuts it
+    if (tm.rank == 0) {
+      const int cnt = sm.list_n;
+      if (cnt == 0 || cnt > kListCap) {
+        if (tid == 0) tm.say(0, 1);
+      } else {
+        sort_list(sm.list, cnt);
+        const int kk = by_k ? (int)ask.k : cnt;  // tokens of the list that top-k leaves
+        // this thread's run of the list and its weight
+        const int run = (cnt + kSmpThreads - 1) / kSmpThreads, i0 = min(cnt, tid * run), i1 = min(cnt, i0 + run);
+        u64 mine = 0;
+        for (int i = i0; i < i1; ++i)
+          if (i < kk) mine += weight(s, sm.tab, key_value(sm.list[i]));
+        u64 all;
+        const u64 at = cta_exclusive(sm, mine, &all);
+        if (ask.by_p) {
+          const u64 total = by_k ? all : Z;
+          const u64 need = share_of(ask.p, total);
+          if (need <= above || need > above + all) {
+            if (tid == 0) tm.say(0, 1);  // the estimate missed
+          } else if (need - above > at && need - above <= at + mine) {
+            u64 c = at;
+            for (int i = i0; i < i1; ++i) {
+              c += i < kk ? weight(s, sm.tab, key_value(sm.list[i])) : 0;
+              if (c >= need - above) {
+                tm.say(sm.list[i], 0);
+                break;
+              }
+            }
+          }
+        } else if (tid == 0) {
+          tm.say(sm.list[kk - 1], 0);
+        }
+      }
+    }
+    const u64* h = tm.heard();
+    if (h[1]) {
+      return false;
+    }
+    const u64 key = h[0];
+    s.vcut = key_value(key);
+    s.idcut = key_index(key);
+    // ---- each CTA's kept weight: what lies above the list, and its own part of it
+    const int cnt = (int)remote_load32(list_n);
+    const int id0 = sl.first, id1 = sl.first + sl.nvec * Elem<T>::kPerVec;
+    for (int i = tid; i < cnt; i += kSmpThreads) {
+      const u64 y = remote_load(list + 8 * i);
+      const int id = key_index(y);
+      if (y < key) break;  // sorted, descending
+      if (id >= id0 && id < id1 && key_value(y) >= s.floor) kept_above += weight(s, sm.tab, key_value(y));
+    }
+    const auto x = tm.tell<false>(kept_above, 0);
+    for (int r = 0; r < tm.size; ++r) {
+      s.total += x[0][r];
+      if (tid == 0) sm.cta_mass[r] = x[0][r];
+    }
+    __syncthreads();
+    return true;
+  }
+}
+
+template <typename T, bool GLOBAL>
+__device__ __forceinline__ void filter_row(Team& tm, const RowSlice<T>& sl, const RowParams& pr, int V, RowStat& s) {
+  if (!cut_by_bins<T, GLOBAL>(tm, sl, pr, V, s)) cut_by_halving<T>(tm, sl, pr, V, s);
 }
 
 // u as the draws read it: NaN and negative as 0, 1 and above as the largest float below 1
 __device__ __forceinline__ double draw_u(float u) { return u >= 0.f ? (double)fminf(u, 0x1.fffffep-1f) : 0.0; }
 
-__device__ __forceinline__ void team_init(Team& tm, SmpShared& sm) {
+__device__ __forceinline__ void team_init(Team& tm, SmpShared& sm, unsigned char* dyn) {
   tm.sm = &sm;
   tm.rank = (int)tm.cl.block_rank();
   tm.size = (int)tm.cl.num_blocks();
   tm.parity = 0;
+  tm.bins = reinterpret_cast<uint32_t*>(dyn);
+  tm.sums = tm.bins + kBinWords;
   if (threadIdx.x < 32) sm.tab[threadIdx.x] = exp2((double)kWeightBits - threadIdx.x / 32.0);
 }
 
+// Draw from the kept tokens of the row: the CTA that thr falls into finds the token.
+template <typename T, typename H>
+__device__ __forceinline__ void draw_kept(Team& tm, const RowSlice<T>& sl, RowStat& s, double u, H&& hit) {
+  SmpShared& sm = *tm.sm;
+  const u64 thr = (u64)(u * (double)s.total);
+  u64 before;
+  if (owner_of(sm.cta_mass, tm.size, thr, before) != tm.rank) return;
+  if (s.idcut < -1) {  // the first so many ties of this slice: find the last one's id
+    select_local<T>(sm, sl, (u64)(-2 - s.idcut) - 1, [&](float x, int) { return (u64)(canon<T>(s, x) == s.vcut); },
+                    [&](int id, float) { sm.pick_id = id; });
+    __syncthreads();
+    s.idcut = sm.pick_id;
+  }
+  select_local<T>(sm, sl, thr - before, [&](float y, int id) {
+                    const float x = canon<T>(s, y);
+                    return kept(s, x, id) ? weight(s, sm.tab, x) : 0ull;
+                  }, [&](int id, float y) { hit(id, canon<T>(s, y)); });
+}
+
 template <typename T>
-__global__ void __launch_bounds__(kSmpThreads)
+__global__ void __launch_bounds__(kSmpThreads, 2)
 sample_kernel(const T* __restrict__ logits, int V, long long stride, eagle_sampling_t params,
               const float* __restrict__ uniforms, int32_t* __restrict__ tokens, float* __restrict__ logprob, int per) {
   __shared__ SmpShared sm;
   extern __shared__ __align__(16) unsigned char dyn[];
   griddep_wait();
   griddep_launch_dependents();
-  Team tm{cg::this_cluster(), &sm, 0, 0, 0};
-  team_init(tm, sm);
+  Team tm{cg::this_cluster(), &sm, nullptr, nullptr, 0, 0, 0};
+  team_init(tm, sm, dyn);
   const long long row = blockIdx.x / tm.size;
   RowSlice<T> sl;
-  sl.vec = reinterpret_cast<uint4*>(dyn);
   place_slice<T>(sl, logits + row * stride, V, per, tm.rank);
-  fill_slice<T>(sl, logits + row * stride, V);
   const RowParams pr = row_params(params, row);
   const float u = uniforms[row];
-  __syncthreads();
   RowStat s;
-  filter_row<T>(tm, sl, pr, V, s);
+  filter_row<T, false>(tm, sl, pr, V, s);
   if (s.total == 0) {
     if (tm.rank == 0 && threadIdx.x == 0) {
       tokens[row] = -1;
       if (logprob) logprob[row] = -INFINITY;
     }
-    tm.cl.sync();
-    return;
+  } else {
+    draw_kept<T>(tm, sl, s, draw_u(u), [&](int id, float x) {
+      tokens[row] = id;
+      if (logprob) {
+        // log of the kept probability: (x - M) / T - ln(S / 2^44)
+        const double z = ((double)x - (double)s.top) * (s.c32 * (kLn2 / 32.0));
+        logprob[row] = (float)(z - log(ldexp((double)s.total, -kWeightBits)));
+      }
+    });
   }
-  const unsigned long long thr = (unsigned long long)(draw_u(u) * (double)s.total);
-  select<T>(tm, sl, thr, [&](float x, int id) { return kept(s, x, id) ? weight(s, sm.tab, x) : 0ull; },
-            [&](int id, float x) {
-              tokens[row] = id;
-              if (logprob) {
-                // log of the kept probability: (x - M) / T - ln(S / 2^44)
-                const double z = ((double)x - (double)s.top) * (s.c32 * (kLn2 / 32.0));
-                logprob[row] = (float)(z - log(ldexp((double)s.total, -kWeightBits)));
-              }
-            });
-  tm.cl.sync();  // no CTA leaves while another may still write to its shared memory
+  cluster_sync();  // no CTA leaves while another may still use its shared memory
 }
 
 // The acceptance walk (accept.cu's rules) with p = the filtered target
@@ -473,16 +970,16 @@ __device__ __forceinline__ double team_sum(Team& tm, WalkShared& ws, double v) {
   if ((int)threadIdx.x < tm.size) {
     double a = 0.0;
     for (int w = 0; w < kSmpWarps; ++w) a += ws.part[w];
-    *tm.cl.map_shared_rank(&ws.xd[tm.parity][tm.rank], threadIdx.x) = a;
+    remote_store(remote(&ws.xd[tm.parity][tm.rank], threadIdx.x), (u64)__double_as_longlong(a));
   }
-  tm.cl.sync();
+  cluster_sync();
   double a = 0.0;
   for (int r = 0; r < tm.size; ++r) a += ws.xd[tm.parity][r];
   return a;
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kSmpThreads)
+__global__ void __launch_bounds__(kSmpThreads, 2)
 accept_sampling_kernel(const T* __restrict__ tgt, const T* __restrict__ dft, const double* __restrict__ dlse, int R, int V,
                        int n, int depth, const int32_t* __restrict__ tokens, const int32_t* __restrict__ parents,
                        const int32_t* __restrict__ draft_row, const float* __restrict__ uniforms,
@@ -493,8 +990,8 @@ accept_sampling_kernel(const T* __restrict__ tgt, const T* __restrict__ dft, con
   extern __shared__ __align__(16) unsigned char dyn[];
   griddep_wait();
   griddep_launch_dependents();
-  Team tm{cg::this_cluster(), &sm, 0, 0, 0};
-  team_init(tm, sm);
+  Team tm{cg::this_cluster(), &sm, nullptr, nullptr, 0, 0, 0};
+  team_init(tm, sm, dyn);
   const int b = blockIdx.x / tm.size, tid = threadIdx.x;
   const bool leader = tm.rank == 0 && tid == 0;
   const size_t trow0 = (size_t)b * (n + 1);
@@ -509,9 +1006,7 @@ accept_sampling_kernel(const T* __restrict__ tgt, const T* __restrict__ dft, con
     ws.u_acc[tid] = uniforms[(size_t)b * 2 * (n + 1) + tid];
   }
   const RowParams pr = row_params(params, b);
-  RowSlice<T> sl, dl;
-  sl.vec = reinterpret_cast<uint4*>(dyn);
-  dl.vec = sl.vec + per;
+  RowSlice<T> sl;
   __syncthreads();
 
   int j = 0, len = 0;
@@ -522,18 +1017,14 @@ accept_sampling_kernel(const T* __restrict__ tgt, const T* __restrict__ dft, con
     const T* drow = r >= 0 ? dft + ((size_t)b * R + r) * (size_t)V : nullptr;
     const double lse = r >= 0 ? dlse[(size_t)b * R + r] : 0.0;
     place_slice<T>(sl, trow, V, per, tm.rank);
-    fill_slice<T>(sl, trow, V);
-    dl.first = sl.first;
-    dl.nvec = sl.nvec;
-    filter_row<T>(tm, sl, pr, V, s);
+    filter_row<T, true>(tm, sl, pr, V, s);
     const double inv_S = s.total ? 1.0 / (double)s.total : 0.0;
     // p and q of every child's token (0 for a token outside the vocabulary)
     if (tid < n && ws.par[tid] == j) {
       const int x = ws.tok[tid];
       double p = 0.0, q = 0.0;
       if (x >= 0 && x < V && r >= 0) {
-        float xt = (float)trow[x];
-        if (s.infinite) xt = xt == INFINITY ? 0.f : -INFINITY;  // as in the slice
+        const float xt = canon<T>(s, (float)trow[x]);
         if (kept(s, xt, x)) p = (double)weight(s, sm.tab, xt) * inv_S;
         q = exp((double)(float)drow[x] - lse);
       }
@@ -542,15 +1033,15 @@ accept_sampling_kernel(const T* __restrict__ tgt, const T* __restrict__ dft, con
     }
     __syncthreads();
     double t = 0.0, F = 1.0, Q = 1.0;  // Q: draft mass not yet rejected at j (1 with replacement)
-    bool rejected = false, spent = false, have_draft = false;
+    bool rejected = false, spent = false;
     int moved = 0;
-    // max(0, p - t q) of a token of this slice (the draft slice lies under the target's)
-    auto residual = [&](float x, int id) {
+    // max(0, p - t q) of a token
+    auto residual = [&](float y, int id) {
+      const float x = canon<T>(s, y);
       if (!kept(s, x, id)) return 0.0;
-      const unsigned long long w = weight(s, sm.tab, x);
+      const u64 w = weight(s, sm.tab, x);
       if (w == 0) return 0.0;
-      const float y = (float)reinterpret_cast<const T*>(dl.vec)[id - dl.first];
-      return fmax(0.0, (double)w * inv_S - t * exp((double)y - lse));
+      return fmax(0.0, (double)w * inv_S - t * exp((double)(float)drow[id] - lse));
     };
     if (len < depth && s.total) {
       int c = 1;
@@ -574,8 +1065,6 @@ accept_sampling_kernel(const T* __restrict__ tgt, const T* __restrict__ dft, con
         ++c;
         while (c <= n && ws.par[c - 1] != j) ++c;
         if (c <= n) {  // another sibling will be tested: F at the new t
-          if (!have_draft) fill_slice<T>(dl, drow, V);
-          have_draft = true;
           double f = 0.0;
           each<T>(sl, [&](float x, int id) { f += residual(x, id); });
           F = team_sum(tm, ws, f);
@@ -599,23 +1088,20 @@ accept_sampling_kernel(const T* __restrict__ tgt, const T* __restrict__ dft, con
     bool drawn = false;
     if (s.total && !spent) {
       if (!rejected) {
-        select<T>(tm, sl, (unsigned long long)(u * (double)s.total),
-                  [&](float x, int id) { return kept(s, x, id) ? weight(s, sm.tab, x) : 0ull; },
-                  [&](int id, float) { bonus[b] = id; });
+        draw_kept<T>(tm, sl, s, u, [&](int id, float) { bonus[b] = id; });
         drawn = true;
       } else {
-        if (!have_draft) fill_slice<T>(dl, drow, V);
         double f = 0.0;
         each<T>(sl, [&](float x, int id) { f += residual(x, id); });
         F = team_sum(tm, ws, f);
         if (F > 0.0) {
           // integer weights of the residual, their sum about 2^60
           const double scale = 1152921504606846976.0 / F;
-          auto g = [&](float x, int id) { return (unsigned long long)(residual(x, id) * scale); };
-          unsigned long long W = 0, unused = 0;
+          auto g = [&](float x, int id) { return (u64)(residual(x, id) * scale); };
+          u64 W = 0, unused = 0;
           each<T>(sl, [&](float x, int id) { W += g(x, id); });
-          tm.sums(W, unused);
-          select<T>(tm, sl, (unsigned long long)(u * (double)W), g, [&](int id, float) { bonus[b] = id; });
+          tm.sums2(W, unused);
+          select<T>(tm, sl, (u64)(u * (double)W), g, [&](int id, float) { bonus[b] = id; });
           drawn = true;
         }
       }
@@ -625,13 +1111,13 @@ accept_sampling_kernel(const T* __restrict__ tgt, const T* __restrict__ dft, con
       if (s.top == -INFINITY) {
         if (leader) bonus[b] = -1;
       } else {
-        select<T>(tm, sl, 0ull, [&](float x, int) { return (unsigned long long)(x == s.top); },
+        select<T>(tm, sl, 0ull, [&](float x, int) { return (u64)(canon<T>(s, x) == s.top); },
                   [&](int id, float) { bonus[b] = id; });
       }
     }
     break;
   }
-  tm.cl.sync();  // no CTA leaves while another may still write to its shared memory
+  cluster_sync();  // no CTA leaves while another may still write to its shared memory
 }
 
 // ------------------------------------------------------------------- host
@@ -659,19 +1145,22 @@ struct RowPlan {
 RowPlan plan_row(long long rows, int V, int elem_bytes) {
   const int E = 16 / elem_bytes;
   const int all = (V + 2 * E - 2) / E;  // a row may start inside its first vector
-  int cl = (all * 16 + kSmpSliceBytes - 1) / kSmpSliceBytes;
+  int cl = 2;
   // few rows: more CTAs each, as long as all fit at two per SM
   const long long want = 2LL * device_sm_count() / rows;
   if (cl < want) cl = (int)(want < kSmpMaxCluster ? want : kSmpMaxCluster);
-  if (cl > kSmpMaxCluster) cl = kSmpMaxCluster;
-  if (cl > all) cl = all;
+  if (cl > (all + kSmpThreads - 1) / kSmpThreads) cl = (all + kSmpThreads - 1) / kSmpThreads;  // a vector per thread at least
   return {cl, (all + cl - 1) / cl};
+}
+// The counts, and the cluster's counts of one CTA's segment.
+size_t bins_bytes(int cluster) {
+  return (kBinWords + align_up((kBins + cluster - 1) / cluster, 4)) * sizeof(uint32_t);
 }
 
 template <typename... KArgs, typename... Args>
 cudaError_t launch_cluster(void (*kernel)(KArgs...), long long grid, int cluster, size_t smem, bool pdl, cudaStream_t s,
                            Args... args) {
-  cudaError_t e = ensure_smem_limit((const void*)kernel, smem + 4096);
+  cudaError_t e = ensure_smem_limit((const void*)kernel, smem);
   if (e == cudaSuccess && cluster > 8) e = ensure_wide_cluster((const void*)kernel);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
@@ -697,7 +1186,7 @@ cudaError_t launch_sample(const void* logits, int dtype, long long rows, int V, 
                           const eagle_sampling_t& params, const float* uniforms, int32_t* tokens, float* logprob,
                           cudaStream_t s) {
   const RowPlan pl = plan_row(rows, V, dtype_bytes(dtype));
-  const size_t smem = (size_t)pl.per * 16;
+  const size_t smem = bins_bytes(pl.cluster);
   if (dtype == EAGLE_F32)
     return launch_cluster(sample_kernel<float>, rows * pl.cluster, pl.cluster, smem, false, s,
                           static_cast<const float*>(logits), V, stride, params, uniforms, tokens, logprob, pl.per);
@@ -711,7 +1200,7 @@ cudaError_t launch_accept_sampling(const void* tgt, int dtype, const void* dft, 
                                    int n, int V, int depth, int32_t* accepted_len, int32_t* path, int32_t* bonus,
                                    bool pdl, cudaStream_t s) {
   const RowPlan pl = plan_row(B, V, dtype_bytes(dtype));
-  const size_t smem = (size_t)pl.per * 32;  // a target and a draft slice
+  const size_t smem = bins_bytes(pl.cluster);
   const long long grid = (long long)B * pl.cluster;
   if (dtype == EAGLE_F32)
     return launch_cluster(accept_sampling_kernel<float>, grid, pl.cluster, smem, pdl, s, static_cast<const float*>(tgt),
