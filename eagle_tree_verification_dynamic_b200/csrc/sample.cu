@@ -58,7 +58,11 @@ constexpr int kPatLow = (127 - 16) << 7, kPatHigh = (127 + 9) << 7;
 constexpr int kZeroBin = kPatHigh - kPatLow + 1;
 constexpr int kLastBin = 2 * kZeroBin;
 constexpr int kBins = kLastBin + 1;
-constexpr int kBinWords = (kBins + 3) / 4 * 4;
+// In shared memory a bin's count sits at its distance from the zero bin, those
+// of negative values kNegative further on.
+constexpr int kNegative = 4096;
+constexpr int kBinWords = 2 * kNegative;
+static_assert(kZeroBin < kNegative, "a slot per bin");
 
 struct SmpShared {
   double tab[32];                   // 2^(44 - j/32)
@@ -67,10 +71,8 @@ struct SmpShared {
   u64 warp_part[2][kSmpWarps];
   u64 cta_mass[kSmpMaxCluster];     // kept weight of each CTA's slice
   u64 list[kListCap];               // CTA 0: (order bits, ~id) of the tokens gathered
-  u64 pick_base;
   int pick_entry, pick_id;
   int list_n;
-  unsigned n_tiny;
 };
 
 // A CTA's slice of a row in global memory: vectors of 16 bytes; element e of
@@ -123,6 +125,10 @@ struct RowStat {
   int idcut;
   float floor;
   u64 total;       // S (0: nothing to draw)
+  // bf16 rows settled by the bins: kept values lie in bins [bin0, bin1] (-1: not settled so); of the tokens equal
+  // to vcut the CTA's slice keeps the first `ties` of its own
+  int bin0, bin1;
+  u64 ties;
 };
 
 // A logit as the passes over the row read it, see RowStat::infinite and merged
@@ -165,6 +171,8 @@ __device__ __forceinline__ int bin_of(uint32_t pat) {
   const int t = min(max((int)(pat & 0x7fffu), kPatLow - 1), kPatHigh) - (kPatLow - 1);
   return (pat & 0x8000u) ? kZeroBin + t : kZeroBin - t;
 }
+__device__ __forceinline__ int slot_of(int j) { return j <= kZeroBin ? kZeroBin - j : kNegative + j - kZeroBin; }
+__device__ __forceinline__ void count_at(uint32_t a) { asm volatile("red.shared.add.u32 [%0], 1;" ::"r"(a) : "memory"); }
 // The pattern of a bin (both ends: beyond the range), as the value whose lower
 // half is `low`: for bf16 (low = 0) the bin's one value.
 __device__ __forceinline__ float bin_value(int j, uint32_t low) {
@@ -227,8 +235,9 @@ __device__ __forceinline__ void cluster_sync() {
 struct Team {
   cg::cluster_group cl;
   SmpShared* sm;
-  uint32_t* bins;  // this CTA's counts [kBinWords]
-  uint32_t* sums;  // the cluster's counts of this CTA's segment of the bins
+  uint32_t* bins;  // this CTA's counts, by slot [kBinWords]
+  uint32_t* sums;  // the cluster's counts of this CTA's segment of the bins (one CTA: unused)
+  uint32_t* lows;  // fp32: per positive slot, the sum of the logits' lower 16 bits (/ 16) [kNegative], then the segment's
   int rank, size, parity;
 
   // Two numbers per CTA (each thread's a and b summed over the CTA, or their
@@ -281,9 +290,9 @@ struct Team {
   }
 };
 
+// f(vector, its index) over the CTA's slice, each(): f(logit, id).
 template <typename T, typename F>
-__device__ __forceinline__ void each(const RowSlice<T>& sl, F&& f) {
-  constexpr int E = Elem<T>::kPerVec;
+__device__ __forceinline__ void each_vec(const RowSlice<T>& sl, F&& f) {
   for (int v0 = threadIdx.x; v0 < sl.nvec; v0 += kSmpThreads * kSmpBatch) {
     uint4 u[kSmpBatch];
 #pragma unroll
@@ -295,22 +304,31 @@ __device__ __forceinline__ void each(const RowSlice<T>& sl, F&& f) {
     for (int i = 0; i < kSmpBatch; ++i) {
       const int v = v0 + i * kSmpThreads;
       if (v >= sl.nvec) break;
-      float x[E];
-      Elem<T>::unpack(u[i], x);
-      const int id = sl.first + v * E;
-#pragma unroll
-      for (int e = 0; e < E; ++e) f(x[e], id + e);
+      f(u[i], v);
     }
   }
+}
+template <typename T, typename F>
+__device__ __forceinline__ void each(const RowSlice<T>& sl, F&& f) {
+  constexpr int E = Elem<T>::kPerVec;
+  each_vec<T>(sl, [&](const uint4& u, int v) {
+    float x[E];
+    Elem<T>::unpack(u, x);
+    const int id = sl.first + v * E;
+#pragma unroll
+    for (int e = 0; e < E; ++e) f(x[e], id + e);
+  });
 }
 
 // All threads of one CTA: the smallest id of its slice whose cumulative g(x, id)
 // (a non-negative integer) exceeds thr, thr < the slice's total: the thread with
-// that token calls hit(id, x).
+// that token calls hit(id, x).  A warp takes up to 512 neighbouring vectors at a
+// time (no barrier in between); those that hold thr are split over the warps
+// again, down to 64 or less, which one warp's lanes share.
 template <typename T, typename G, typename H>
 __device__ __forceinline__ void select_local(SmpShared& sm, const RowSlice<T>& sl, u64 thr, G&& g, H&& hit) {
   constexpr int E = Elem<T>::kPerVec;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   auto vec_sum = [&](const uint4& u, int v) {
     float y[E];
     Elem<T>::unpack(u, y);
@@ -319,54 +337,87 @@ __device__ __forceinline__ void select_local(SmpShared& sm, const RowSlice<T>& s
     for (int e = 0; e < E; ++e) s += g(y[e], sl.first + v * E + e);
     return s;
   };
-  // ids ascend with the round (256 vectors), the warp and the lane: find the
-  // round and warp first
+  auto region_sum = [&](int v0, int count) {  // of the warp, count a multiple of 32
+    u64 s = 0;
+    for (int i = 0; i < count; i += 32 * kSmpBatch) {
+      uint4 u[kSmpBatch];
+#pragma unroll
+      for (int q = 0; q < kSmpBatch; ++q) {
+        const int v = v0 + i + q * 32 + lane;
+        u[q] = v < sl.nvec && i + q * 32 < count ? sl.get(v) : Elem<T>::neg_inf_vec();
+      }
+#pragma unroll
+      for (int q = 0; q < kSmpBatch; ++q) {
+        const int v = v0 + i + q * 32 + lane;
+        if (v < sl.nvec && i + q * 32 < count) s += vec_sum(u[q], v);
+      }
+    }
+    return warp_sum_u64(s);
+  };
+  // the part of list[0..8) that holds thr (kSmpWarps: none); base becomes what lies before it
   u64 base = 0;
-  const int rounds = (sl.nvec + kSmpThreads - 1) / kSmpThreads;
-  int entry = -1;
-  for (int q0 = 0; q0 < rounds; q0 += kSmpBatch) {
-    uint4 u[kSmpBatch];
+  auto part_of = [&](const u64* parts) {
+    int at = kSmpWarps;
+    u64 run = base;
 #pragma unroll
-    for (int i = 0; i < kSmpBatch; ++i) {
-      const int v = (q0 + i) * kSmpThreads + tid;
-      u[i] = v < sl.nvec ? sl.get(v) : Elem<T>::neg_inf_vec();
+    for (int w = 0; w < kSmpWarps; ++w) {
+      const u64 y = parts[w];
+      if (at == kSmpWarps && thr < run + y) {
+        at = w;
+        base = run;
+      }
+      run += y;
     }
-#pragma unroll
-    for (int i = 0; i < kSmpBatch; ++i) {
-      const int v = (q0 + i) * kSmpThreads + tid;
-      const u64 s = warp_sum_u64(v < sl.nvec ? vec_sum(u[i], v) : 0);
-      if (lane == 0) sm.list[i * kSmpWarps + warp] = s;
-    }
+    if (at == kSmpWarps) base = run;
+    return at;
+  };
+  u64* parts = sm.list;
+  int v0 = -1, owner = 0;
+  int region = sl.nvec <= kSmpWarps * 32 ? 32 : (sl.nvec <= kSmpWarps * 64 ? 64 : (sl.nvec <= kSmpWarps * 256 ? 256 : 512));
+  for (int b = 0; b < sl.nvec; b += kSmpWarps * region) {
+    const u64 s = b + warp * region < sl.nvec ? region_sum(b + warp * region, region) : 0;
+    if (lane == 0) parts[warp] = s;
     __syncthreads();
-    const u64 c = sm.list[lane];  // kSmpBatch * kSmpWarps = 32 entries, in id order
-    static_assert(kSmpBatch * kSmpWarps == 32, "one entry per lane");
-    const u64 inc = warp_scan_u64(c);
-    const unsigned m = __ballot_sync(kFull, thr < base + inc);
-    if (m) {
-      const int src = __ffs(m) - 1;
-      entry = q0 * kSmpWarps + src;
-      base += __shfl_sync(kFull, inc - c, src);
+    const int at = part_of(parts);
+    __syncthreads();
+    if (at < kSmpWarps) {
+      v0 = b + at * region;
+      owner = at;
       break;
     }
-    base += __shfl_sync(kFull, inc, 31);
-    __syncthreads();
   }
-  if (entry < 0 || entry % kSmpWarps != warp) return;
-  const int v = entry / kSmpWarps * kSmpThreads + tid;
-  const uint4 u = v < sl.nvec ? sl.get(v) : Elem<T>::neg_inf_vec();
-  const u64 c = v < sl.nvec ? vec_sum(u, v) : 0;
-  u64 cum = base + warp_scan_u64(c) - c;
-  if (thr < cum || thr >= cum + c) return;
-  float y[E];
-  Elem<T>::unpack(u, y);
-  bool done = false;
+  if (v0 < 0) return;  // (thr is below the total)
+  if (region > 64) {
+    region /= kSmpWarps;
+    const u64 s = region_sum(v0 + warp * region, region);
+    if (lane == 0) parts[warp] = s;
+    __syncthreads();
+    const int at = part_of(parts);
+    __syncthreads();
+    v0 += at * region;
+    owner = at;
+  }
+  if (owner != warp) return;
+  for (int i = 0; i < region; i += 32) {
+    const int v = v0 + i + lane;
+    const uint4 u = v < sl.nvec ? sl.get(v) : Elem<T>::neg_inf_vec();
+    const u64 c = v < sl.nvec ? vec_sum(u, v) : 0;
+    const u64 inc = warp_scan_u64(c);
+    u64 cum = base + inc - c;
+    if (thr >= cum && thr < cum + c) {
+      float y[E];
+      Elem<T>::unpack(u, y);
+      bool done = false;
 #pragma unroll
-  for (int e = 0; e < E; ++e) {
-    cum += g(y[e], sl.first + v * E + e);
-    if (!done && thr < cum) {
-      done = true;
-      hit(sl.first + v * E + e, y[e]);
+      for (int e = 0; e < E; ++e) {
+        cum += g(y[e], sl.first + v * E + e);
+        if (!done && thr < cum) {
+          done = true;
+          hit(sl.first + v * E + e, y[e]);
+        }
+      }
     }
+    base += __shfl_sync(kFull, inc, 31);
   }
 }
 
@@ -390,6 +441,8 @@ __device__ __forceinline__ void select(Team& tm, const RowSlice<T>& sl, u64 thr,
 }
 
 // ------------------------------------------------------------ a row's cut
+constexpr int kTieUnknown = -2;
+
 struct RowParams {
   float temperature, top_p, min_p;
   int top_k;
@@ -443,6 +496,7 @@ template <typename T>
 __device__ __forceinline__ void cut_by_halving(Team& tm, const RowSlice<T>& sl, const RowParams& pr, int V, RowStat& s) {
   SmpShared& sm = *tm.sm;
   s.infinite = s.merged = false;
+  s.bin0 = s.bin1 = -1;
   s.total = 0;
   {
     float m = -INFINITY;
@@ -525,11 +579,11 @@ __device__ __forceinline__ u64 cta_exclusive(SmpShared& sm, u64 mine, u64* all) 
 }
 
 // The first bin (in descending order of value) at which the running measure of
-// the cluster reaches `need`; per bin `of(j, count)`, per CTA the measure `seg`
-// of its segment, this thread's part `mine` of it (bins [j0, j1)).  Exactly one
+// the cluster reaches `need`; per bin `of(j)`, per CTA the measure `seg`
+// of its segment, this thread's part `mine` of it (bins [j0, j1)).  One
 // thread of the cluster calls found(bin, measure before it) if need is reached.
 template <typename O, typename F>
-__device__ __forceinline__ void find_bin(Team& tm, const u64* seg, u64 need, u64 mine, int j0, int j1, int seg0, O&& of,
+__device__ __forceinline__ void find_bin(Team& tm, const u64* seg, u64 need, u64 mine, int j0, int j1, O&& of,
                                          F&& found) {
   u64 before;
   if (owner_of(seg, tm.size, need - 1, before) != tm.rank) return;
@@ -538,7 +592,7 @@ __device__ __forceinline__ void find_bin(Team& tm, const u64* seg, u64 need, u64
   u64 run = at;
   if (need > at && need <= at + mine) {
     for (int j = j0; j < j1 && hit < 0; ++j) {
-      const u64 m = of(j, tm.sums[j - seg0]);
+      const u64 m = of(j);
       if (need <= run + m) hit = j;
       else run += m;
     }
@@ -578,21 +632,54 @@ __device__ __forceinline__ bool cut_by_bins(Team& tm, const RowSlice<T>& sl, con
   constexpr bool kExact = sizeof(T) == 2;  // a bin is one value
   s.infinite = false;
   s.merged = kExact;
+  s.bin0 = s.bin1 = -1;
+  s.ties = ~0ull;
   s.vcut = s.floor = -INFINITY;
   s.idcut = 0x7fffffff;
   s.total = 0;
   // ---- counts by value
+  // (fp32 needs the places inside a bin only to estimate weights)
+  const bool placed = !kExact && pr.temperature > 0.f && pr.top_p < 1.f;
   for (int i = tid; i < kBinWords / 4; i += kSmpThreads) reinterpret_cast<uint4*>(tm.bins)[i] = make_uint4(0, 0, 0, 0);
+  if (placed)
+    for (int i = tid; i < kNegative / 4; i += kSmpThreads) reinterpret_cast<uint4*>(tm.lows)[i] = make_uint4(0, 0, 0, 0);
   if (tid == 0) {
     sm.list_n = 0;
-    sm.n_tiny = 0;
+    sm.pick_entry = 0;
   }
   __syncthreads();
   float m = -INFINITY;
-  each<T>(sl, [&](float x, int) {
-    atomicAdd(tm.bins + bin_of(__float_as_uint(x) >> 16), 1u);
-    if (!kExact) m = fmaxf(m, x);
+  const uint32_t bins_at = (uint32_t)__cvta_generic_to_shared(tm.bins);
+  each_vec<T>(sl, [&](const uint4& u, int) {
+    const uint32_t word[4] = {u.x, u.y, u.z, u.w};
+    if constexpr (kExact) {
+      // two logits at a time: magnitudes clamped to the bins' range, their
+      // distances from its low end, the sign as the slots' upper half, as the
+      // lower halves of shared-memory addresses (the upper half names the CTA)
+      constexpr uint32_t kLow2 = (kPatLow - 1) * 0x10001u, kHigh2 = kPatHigh * 0x10001u;
+      const uint32_t base2 = (bins_at & 0xffffu) * 0x10001u;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t w = word[i];
+        const uint32_t t = __vminu2(__vmaxu2(w & 0x7fff7fffu, kLow2), kHigh2) - kLow2;
+        const uint32_t a = ((t | ((w >> 3) & (kNegative * 0x10001u))) << 2) + base2;
+        count_at(__byte_perm(a, bins_at, 0x7610));
+        count_at(__byte_perm(a, bins_at, 0x7632));
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t w = word[i];
+        const int t = min(max((int)((w >> 16) & 0x7fffu), kPatLow - 1), kPatHigh) - (kPatLow - 1);
+        count_at(bins_at + 4u * ((uint32_t)t | ((w >> 19) & kNegative)));
+        m = fmaxf(m, __uint_as_float(w));
+        // (negative logits are only ever estimated roughly)
+        if (placed && !(w >> 31)) atomicAdd(tm.lows + t, (w & 0xffffu) >> 4);
+      }
+    }
   });
+  __syncthreads();
+  if (tid == 0) tm.bins[0] += tm.bins[kNegative];  // both zeros
   // (padding reads as -inf: it only adds to the last bin, which is never used)
   cluster_sync();
   // ---- this CTA's segment of the bins, summed over the cluster
@@ -602,8 +689,20 @@ __device__ __forceinline__ bool cut_by_bins(Team& tm, const RowSlice<T>& sl, con
   u64 first = 0;  // order bits of the largest value counted
   for (int j = j0; j < j1; ++j) {
     uint32_t c = 0;
-    for (int r = 0; r < tm.size; ++r) c += remote_load32(remote(tm.bins + j, r));
-    tm.sums[j - seg0] = c;
+    const int at = slot_of(j);
+    if (tm.size == 1) {
+      c = tm.bins[at];
+    } else {
+#pragma unroll 4
+      for (int r = 0; r < tm.size; ++r) c += remote_load32(remote(tm.bins + at, r));
+      tm.sums[j - seg0] = c;
+      if (placed && c && j < kZeroBin) {
+        uint32_t l = 0;
+#pragma unroll 4
+        for (int r = 0; r < tm.size; ++r) l += remote_load32(remote(tm.lows + at, r));
+        tm.lows[kNegative + j - seg0] = l;
+      }
+    }
     if (c && !first && j < kLastBin) first = order_bits(j == 0 ? INFINITY : bin_value(j, 0));
   }
   {
@@ -620,6 +719,7 @@ __device__ __forceinline__ bool cut_by_bins(Team& tm, const RowSlice<T>& sl, con
     }
     s.top = kExact ? lead : order_value((uint32_t)b);
   }
+  auto sum_at = [&](int j) { return tm.size == 1 ? tm.bins[slot_of(j)] : tm.sums[j - seg0]; };
   const RowAsk ask = row_ask(pr, V, s);
   if (!((s.top + 512.f) * s.c >= 45.5f)) {  // tokens of the last bin would weigh something
     u64 n = 0, unused = 0;
@@ -635,12 +735,13 @@ __device__ __forceinline__ bool cut_by_bins(Team& tm, const RowSlice<T>& sl, con
     auto count_of = [&](int j, uint32_t c) { return j < kLastBin ? (u64)c : 0ull; };
     u64 n = 0, w = 0;
     for (int j = j0; j < j1; ++j) {
-      const uint32_t c = tm.sums[j - seg0];
+      const uint32_t c = sum_at(j);
       n += count_of(j, c);
       if (ask.by_p) w += mass_of(j, c);
     }
     u64 ties = ~0ull;  // of the tokens equal to s.vcut
     int cut_bin = kLastBin;
+    u64 zero_in = 0;  // a sum that the zero bin took part in
     if (ask.k > 0 || ask.by_p) {
       const auto x = tm.tell<false>(n, w);
       u64 N = 0, Z = 0;
@@ -649,7 +750,7 @@ __device__ __forceinline__ bool cut_by_bins(Team& tm, const RowSlice<T>& sl, con
         Z += x[1][r];
       }
       if (ask.k > 0 && N > (u64)ask.k) {
-        find_bin(tm, x[0], (u64)ask.k, n, j0, j1, seg0, count_of, [&](int j, u64 at) {
+        find_bin(tm, x[0], (u64)ask.k, n, j0, j1, [&](int j) { return count_of(j, sum_at(j)); }, [&](int j, u64 at) {
           // the tokens above the bin, and how many of it
           tm.say((u64)j, (u64)ask.k - at);
         });
@@ -659,15 +760,16 @@ __device__ __forceinline__ bool cut_by_bins(Team& tm, const RowSlice<T>& sl, con
         if (ask.by_p) {
           // Z: the weight above the bin, and the ties'
           u64 above = 0, unused = 0;
-          for (int j = j0; j < min(j1, cut_bin); ++j) above += mass_of(j, tm.sums[j - seg0]);
+          for (int j = j0; j < min(j1, cut_bin); ++j) above += mass_of(j, sum_at(j));
           tm.sums2(above, unused);
           Z = above + ties * weight(s, sm.tab, bin_value(cut_bin, 0));
         }
       }
       if (ask.by_p) {
+        if (cut_bin >= kZeroBin) zero_in = Z;  // the zero bin is part of Z
         const u64 need = share_of(ask.p, Z);
         const auto y = tm.tell<false>(n, w);
-        find_bin(tm, y[1], need, w, j0, j1, seg0, mass_of, [&](int j, u64 at) {
+        find_bin(tm, y[1], need, w, j0, j1, [&](int j) { return mass_of(j, sum_at(j)); }, [&](int j, u64 at) {
           const u64 one = weight(s, sm.tab, bin_value(j, 0));
           tm.say((u64)j, (need - at + one - 1) / one);
         });
@@ -678,61 +780,68 @@ __device__ __forceinline__ bool cut_by_bins(Team& tm, const RowSlice<T>& sl, con
       if (cut_bin < kLastBin) s.vcut = bin_value(cut_bin, 0);
     }
     s.floor = ask.floor;
-    // values read as 0 must not show: neither in a sum nor by a cut among them
+    // ---- each CTA's kept weight, from its own counts
     {
-      const u64 zeros = tm.bins[kZeroBin];
-      u64 tiny = 0;
-      if (zeros)
-        each<T>(sl, [&](float x, int) { tiny += x != 0.f && fabsf(x) < 0x1p-16f; });
-      u64 a = 0, mine = 0;
-      // ---- each CTA's kept weight, from its own counts
+      u64 mine = 0;
       const int from = bin_of(__float_as_uint(s.top) >> 16);
+      int last = from;  // the last bin kept
       for (int j = from + tid; j < cut_bin; j += kSmpThreads) {
-        const uint32_t c = tm.bins[j];
-        if (c == 0) continue;
+        const uint32_t c = tm.bins[slot_of(j)];
         const float v = bin_value(j, 0);
-        if (v < s.floor) break;
-        mine += c * weight(s, sm.tab, v);
+        if (v < s.floor || !((s.top - v) * s.c < 45.5f)) break;
+        last = j;
+        if (c) mine += c * weight(s, sm.tab, v);
       }
-      a = (tid == 0 && cut_bin < kLastBin ? (u64)tm.bins[cut_bin] : 0ull) + (tiny << 32);
+      last = __reduce_max_sync(kFull, last);
+      if ((tid & 31) == 0) atomicMax(&sm.pick_entry, last);  // (set to 0 above)
+      const u64 a = tid == 0 && cut_bin < kLastBin ? (u64)tm.bins[slot_of(cut_bin)] : 0ull;
       const auto x = tm.tell<false>(mine, a);
       const bool at_floor = cut_bin < kLastBin && s.vcut >= s.floor;  // the tokens equal to the cut are kept
       const u64 one = at_floor ? weight(s, sm.tab, s.vcut) : 0ull;
-      u64 seen = 0, my_ties = 0, tiny_all = 0;
+      u64 seen = 0, my_ties = 0, before_me = 0;
       s.total = 0;
       for (int r = 0; r < tm.size; ++r) {
-        const u64 eq = x[1][r] & 0xffffffffull;
+        const u64 eq = x[1][r];
         const u64 take = ties > seen ? (ties - seen < eq ? ties - seen : eq) : 0;
-        tiny_all += x[1][r] >> 32;
-        if (r == tm.rank) my_ties = take;
+        if (r == tm.rank) {
+          my_ties = take;
+          before_me = seen;
+        }
         const u64 mass = x[0][r] + take * one;
         if (tid == 0) sm.cta_mass[r] = mass;
         s.total += mass;
         seen += eq;
       }
       __syncthreads();
-      // a value below 2^-16 read as 0 is off by at most 2^-16 c of its weight
-      if (tiny_all &&
-          (cut_bin == kZeroBin || !((double)tiny_all * (double)weight(s, sm.tab, 0.f) * (double)s.c * 0x1p-16 <= (double)s.total * 0x1p-32))) {
-        return false;
+      s.bin0 = from;
+      s.bin1 = at_floor ? cut_bin : sm.pick_entry;
+      s.ties = my_ties;
+      // Values below 2^-16 are read as 0, off by at most 2^-16 c of their weight:
+      // that must not show in a sum (2^-32 of it), nor by a cut among them
+      if (cut_bin > kZeroBin && s.floor <= 0.f && (zero_in == 0 || s.total < zero_in)) zero_in = s.total;
+      if (zero_in || cut_bin == kZeroBin) {
+        u64 tiny = 0, unused = 0;
+        if (tm.bins[0])
+          each<T>(sl, [&](float y, int) { tiny += y != 0.f && fabsf(y) < 0x1p-16f; });
+        tm.sums2(tiny, unused);
+        if (tiny && (cut_bin == kZeroBin ||
+                     !((double)tiny * (double)weight(s, sm.tab, 0.f) * (double)s.c * 0x1p-16 <= (double)zero_in * 0x1p-32)))
+          return false;
       }
       if (cut_bin < kLastBin && ties < seen) {
         // some of the tokens equal to the cut: by id, so all in the CTAs before
         // one, none in those after it
-        const u64 eq = tm.bins[cut_bin];
+        const u64 eq = tm.bins[slot_of(cut_bin)];
         auto is_tie = [&](float x2, int) { return (u64)(canon<T>(s, x2) == s.vcut); };
         if constexpr (GLOBAL) {
           // the CTA that holds the last tie taken finds its id for all
-          u64 before = 0;
-          for (int r = 0; r < tm.rank; ++r) before += x[1][r] & 0xffffffffull;
-          if (ties > before && ties <= before + eq)
-            select_local<T>(sm, sl, ties - before - 1, is_tie, [&](int id, float) { tm.say((u64)id, 0); });
+          if (my_ties > 0 && (my_ties < eq || ties == before_me + eq))
+            select_local<T>(sm, sl, my_ties - 1, is_tie, [&](int id, float) { tm.say((u64)id, 0); });
           s.idcut = (int)tm.heard()[0];
         } else if (my_ties == 0) {
           s.idcut = -1;
         } else if (my_ties < eq) {
-          // (looked up by the CTA that the draw falls into, see sample_kernel)
-          s.idcut = -2 - (int)my_ties;
+          s.idcut = kTieUnknown;  // looked up by the CTA that the draw falls into, see draw_kept
         }
       }
     }
@@ -740,14 +849,19 @@ __device__ __forceinline__ bool cut_by_bins(Team& tm, const RowSlice<T>& sl, con
   } else {
     // ---- fp32: exact sums and a list around the cut, in a second pass
     auto count_of = [&](int j, uint32_t c) { return j < kLastBin ? (u64)c : 0ull; };
-    auto guess_of = [&](int j, uint32_t c) {  // weight of the bin's middle, the bin's at half a percent or so
+    // a bin's weight, estimated: its tokens at their mean place, and what their
+    // spread adds to the mean of an exponential (variance width^2 / 12)
+    auto guess_of = [&](int j, uint32_t c) {
       if (!c || j == 0 || j >= kLastBin) return 0ull;
-      const float v = bin_value(j, 0x8000u);
-      return c * weight(s, sm.tab, v < s.top ? v : s.top);
+      const uint32_t mean = j < kZeroBin ? min(0xffffu, (tm.size == 1 ? tm.lows[slot_of(j)] : tm.lows[kNegative + j - seg0]) / c * 16 + 8) : 0x8000u;
+      const float v = bin_value(j, mean);
+      const u64 w1 = weight(s, sm.tab, v < s.top ? v : s.top);
+      const float wide = (bin_value(j, 0xffffu) - bin_value(j, 0)) * (s.c * (float)kLn2);
+      return (u64)((double)c * (double)w1 * (c > 1 ? 1.0 + (double)fminf(wide * wide, 1.f) / 24.0 : 1.0));
     };
     u64 n = 0, w = 0;
     for (int j = j0; j < j1; ++j) {
-      const uint32_t c = tm.sums[j - seg0];
+      const uint32_t c = sum_at(j);
       n += count_of(j, c);
       if (ask.by_p) w += guess_of(j, c);
     }
@@ -763,22 +877,27 @@ __device__ __forceinline__ bool cut_by_bins(Team& tm, const RowSlice<T>& sl, con
       by_k = ask.k > 0 && N > (u64)ask.k;
       window = ask.by_p && !by_k;
       if (by_k) {
-        find_bin(tm, x[0], (u64)ask.k, n, j0, j1, seg0, count_of,
-                 [&](int j, u64 at) { tm.say((u64)j, at + tm.sums[j - seg0]); });
+        find_bin(tm, x[0], (u64)ask.k, n, j0, j1, [&](int j) { return count_of(j, sum_at(j)); },
+                 [&](int j, u64 at) { tm.say((u64)j, at + sum_at(j)); });
         const u64* h = tm.heard();
         hi_bin = (int)h[0];
         slow = h[1] > (u64)kListCap;
       } else if (window) {
         // the bins where the estimated share may be reached, the estimate taken
-        // to be within 1 part in 64 of what remains on either side
+        // to be within 1 part in 128 of what remains on either side
         const u64 need = share_of(ask.p, Zg), rest = Zg - need;
-        const u64 slack = (need < rest ? need : rest) / 64;
+        const u64 slack = (need < rest ? need : rest) / 128;
         const u64 lo = need > slack ? need - slack : 1, hi = need + slack;
-        find_bin(tm, x[1], lo, w, j0, j1, seg0, guess_of, [&](int j, u64) { tm.say((u64)j, 0); });
+        find_bin(tm, x[1], lo, w, j0, j1, [&](int j) { return guess_of(j, sum_at(j)); }, [&](int j, u64) { tm.say((u64)j, 0); });
         lo_bin = (int)tm.heard()[0];
         const auto y = tm.tell<false>(n, w);
-        find_bin(tm, y[1], hi, w, j0, j1, seg0, guess_of, [&](int j, u64) { tm.say((u64)j, 0); });
+        find_bin(tm, y[1], hi, w, j0, j1, [&](int j) { return guess_of(j, sum_at(j)); }, [&](int j, u64) { tm.say((u64)j, 0); });
         hi_bin = (int)tm.heard()[0];
+        // few tokens up to there: list them all, so that nothing depends on the estimate's lower end
+        u64 upto = 0, unused = 0;
+        for (int j = j0; j < min(j1, hi_bin + 1); ++j) upto += sum_at(j);
+        tm.sums2(upto, unused);
+        if (upto <= (u64)kListCap) lo_bin = 0;
       }
     }
     if (slow) {
@@ -889,24 +1008,100 @@ __device__ __forceinline__ void team_init(Team& tm, SmpShared& sm, unsigned char
   tm.size = (int)tm.cl.num_blocks();
   tm.parity = 0;
   tm.bins = reinterpret_cast<uint32_t*>(dyn);
+  // one CTA per row: its counts are the cluster's
+  const int seg = tm.size > 1 ? ((kBins + tm.size - 1) / tm.size + 3) / 4 * 4 : 0;
   tm.sums = tm.bins + kBinWords;
+  tm.lows = tm.bins + kBinWords + seg;
   if (threadIdx.x < 32) sm.tab[threadIdx.x] = exp2((double)kWeightBits - threadIdx.x / 32.0);
 }
 
-// Draw from the kept tokens of the row: the CTA that thr falls into finds the token.
-template <typename T, typename H>
-__device__ __forceinline__ void draw_kept(Team& tm, const RowSlice<T>& sl, RowStat& s, double u, H&& hit) {
+// Where few values are kept (bf16, all positive), the CTA first counts them by
+// sub-slice: counts again make exact weights, one per value instead of one per
+// token, and the draw reads only one sub-slice token by token.  Narrows sl, thr
+// and s.ties to it.
+template <typename T>
+__device__ __forceinline__ void narrow(Team& tm, RowSlice<T>& sl, RowStat& s, u64& thr) {
   SmpShared& sm = *tm.sm;
-  const u64 thr = (u64)(u * (double)s.total);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int nb = s.bin1 - s.bin0 + 1;
+  constexpr int kSubs = 64;  // at most; their weights and the values' share sm.list
+  const int subs = min(min(kSubs, kBinWords / nb), sl.nvec / 64);
+  if (subs < 4 || nb > kListCap - kSubs || s.bin1 >= kZeroBin) return;
+  const int vps = (sl.nvec + subs - 1) / subs;  // vectors per sub-slice
+  __syncthreads();
+  for (int i = tid; i < subs * nb; i += kSmpThreads) tm.bins[i] = 0;
+  u64* wt = sm.list + kSubs;
+  for (int i = tid; i < nb; i += kSmpThreads) wt[i] = weight(s, sm.tab, bin_value(s.bin1 - i, 0));
+  __syncthreads();
+  // a kept logit's pattern, as a signed 16-bit number, is at least the last kept bin's
+  const int low = (int)(__float_as_uint(bin_value(s.bin1, 0)) >> 16);
+  for (int q = warp; q < subs; q += kSmpWarps) {
+    const uint32_t base = (uint32_t)__cvta_generic_to_shared(tm.bins + q * nb);
+    const int end = min((q + 1) * vps, sl.nvec);
+    for (int v0 = q * vps + lane; v0 < end; v0 += 32 * kSmpBatch) {
+      uint4 u[kSmpBatch];
+#pragma unroll
+      for (int i = 0; i < kSmpBatch; ++i) u[i] = v0 + 32 * i < end ? sl.get(v0 + 32 * i) : Elem<T>::neg_inf_vec();
+#pragma unroll
+      for (int i = 0; i < kSmpBatch; ++i) {
+        const uint32_t word[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int a = ((int)(word[k] << 16) >> 16) - low, b = ((int)word[k] >> 16) - low;
+          if (a >= 0) count_at(base + 4u * a);
+          if (b >= 0) count_at(base + 4u * b);
+        }
+      }
+    }
+  }
+  __syncthreads();
+  const bool cut = bin_value(s.bin1, 0) == s.vcut;  // then the first count is of ties
+  for (int q = warp; q < subs; q += kSmpWarps) {
+    u64 m = 0;
+    for (int i = lane + (cut ? 1 : 0); i < nb; i += 32) m += tm.bins[q * nb + i] * wt[i];
+    m = warp_sum_u64(m);
+    if (lane == 0) sm.list[q] = m;
+  }
+  __syncthreads();
+  u64 run = 0, ties = s.ties;
+  int at = subs - 1;
+  for (int q = 0; q < subs; ++q) {
+    const u64 eq = cut ? tm.bins[q * nb] : 0ull;
+    const u64 take = ties < eq ? ties : eq;
+    const u64 m = sm.list[q] + take * (cut ? wt[0] : 0ull);
+    if (thr < run + m) {
+      at = q;
+      if (s.idcut == kTieUnknown) s.idcut = take == eq ? 0x7fffffff : (take == 0 ? -1 : kTieUnknown);
+      s.ties = take;
+      break;
+    }
+    run += m;
+    ties -= take;
+  }
+  thr -= run;
+  sl.first += at * vps * Elem<T>::kPerVec;
+  sl.nvec = min(vps, sl.nvec - at * vps);
+  __syncthreads();
+}
+
+// Draw from the kept tokens of the row: the CTA that the draw falls into finds the token.
+template <typename T, typename H>
+__device__ __forceinline__ void draw_kept(Team& tm, RowSlice<T> sl, RowStat s, double u, H&& hit) {
+  SmpShared& sm = *tm.sm;
+  u64 thr = (u64)(u * (double)s.total);
   u64 before;
   if (owner_of(sm.cta_mass, tm.size, thr, before) != tm.rank) return;
-  if (s.idcut < -1) {  // the first so many ties of this slice: find the last one's id
-    select_local<T>(sm, sl, (u64)(-2 - s.idcut) - 1, [&](float x, int) { return (u64)(canon<T>(s, x) == s.vcut); },
+  thr -= before;
+  if constexpr (sizeof(T) == 2) {
+    if (s.bin0 >= 0) narrow<T>(tm, sl, s, thr);
+  }
+  if (s.idcut == kTieUnknown) {  // the first s.ties ties of this slice: find the last one's id
+    select_local<T>(sm, sl, s.ties - 1, [&](float x, int) { return (u64)(canon<T>(s, x) == s.vcut); },
                     [&](int id, float) { sm.pick_id = id; });
     __syncthreads();
     s.idcut = sm.pick_id;
   }
-  select_local<T>(sm, sl, thr - before, [&](float y, int id) {
+  select_local<T>(sm, sl, thr, [&](float y, int id) {
                     const float x = canon<T>(s, y);
                     return kept(s, x, id) ? weight(s, sm.tab, x) : 0ull;
                   }, [&](int id, float y) { hit(id, canon<T>(s, y)); });
@@ -920,7 +1115,7 @@ sample_kernel(const T* __restrict__ logits, int V, long long stride, eagle_sampl
   extern __shared__ __align__(16) unsigned char dyn[];
   griddep_wait();
   griddep_launch_dependents();
-  Team tm{cg::this_cluster(), &sm, nullptr, nullptr, 0, 0, 0};
+  Team tm{cg::this_cluster(), &sm, nullptr, nullptr, nullptr, 0, 0, 0};
   team_init(tm, sm, dyn);
   const long long row = blockIdx.x / tm.size;
   RowSlice<T> sl;
@@ -990,7 +1185,7 @@ accept_sampling_kernel(const T* __restrict__ tgt, const T* __restrict__ dft, con
   extern __shared__ __align__(16) unsigned char dyn[];
   griddep_wait();
   griddep_launch_dependents();
-  Team tm{cg::this_cluster(), &sm, nullptr, nullptr, 0, 0, 0};
+  Team tm{cg::this_cluster(), &sm, nullptr, nullptr, nullptr, 0, 0, 0};
   team_init(tm, sm, dyn);
   const int b = blockIdx.x / tm.size, tid = threadIdx.x;
   const bool leader = tm.rank == 0 && tid == 0;
@@ -1145,22 +1340,24 @@ struct RowPlan {
 RowPlan plan_row(long long rows, int V, int elem_bytes) {
   const int E = 16 / elem_bytes;
   const int all = (V + 2 * E - 2) / E;  // a row may start inside its first vector
-  int cl = 2;
+  int cl = 1;
   // few rows: more CTAs each, as long as all fit at two per SM
   const long long want = 2LL * device_sm_count() / rows;
   if (cl < want) cl = (int)(want < kSmpMaxCluster ? want : kSmpMaxCluster);
   if (cl > (all + kSmpThreads - 1) / kSmpThreads) cl = (all + kSmpThreads - 1) / kSmpThreads;  // a vector per thread at least
   return {cl, (all + cl - 1) / cl};
 }
-// The counts, and the cluster's counts of one CTA's segment.
-size_t bins_bytes(int cluster) {
-  return (kBinWords + align_up((kBins + cluster - 1) / cluster, 4)) * sizeof(uint32_t);
+// The counts and the cluster's counts of one CTA's segment; for fp32 the places too.
+size_t bins_bytes(int cluster, int elem_bytes) {
+  const size_t seg = cluster > 1 ? align_up((kBins + cluster - 1) / cluster, 4) : 0;
+  return (kBinWords + seg + (elem_bytes == 4 ? kNegative + seg : 0)) * sizeof(uint32_t);
 }
 
 template <typename... KArgs, typename... Args>
 cudaError_t launch_cluster(void (*kernel)(KArgs...), long long grid, int cluster, size_t smem, bool pdl, cudaStream_t s,
                            Args... args) {
-  cudaError_t e = ensure_smem_limit((const void*)kernel, smem);
+  // (the limit without opting in counts the static shared memory too, at most 16 KB here)
+  cudaError_t e = ensure_smem_limit((const void*)kernel, smem + 16 * 1024);
   if (e == cudaSuccess && cluster > 8) e = ensure_wide_cluster((const void*)kernel);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
@@ -1186,7 +1383,7 @@ cudaError_t launch_sample(const void* logits, int dtype, long long rows, int V, 
                           const eagle_sampling_t& params, const float* uniforms, int32_t* tokens, float* logprob,
                           cudaStream_t s) {
   const RowPlan pl = plan_row(rows, V, dtype_bytes(dtype));
-  const size_t smem = bins_bytes(pl.cluster);
+  const size_t smem = bins_bytes(pl.cluster, dtype_bytes(dtype));
   if (dtype == EAGLE_F32)
     return launch_cluster(sample_kernel<float>, rows * pl.cluster, pl.cluster, smem, false, s,
                           static_cast<const float*>(logits), V, stride, params, uniforms, tokens, logprob, pl.per);
@@ -1200,7 +1397,7 @@ cudaError_t launch_accept_sampling(const void* tgt, int dtype, const void* dft, 
                                    int n, int V, int depth, int32_t* accepted_len, int32_t* path, int32_t* bonus,
                                    bool pdl, cudaStream_t s) {
   const RowPlan pl = plan_row(B, V, dtype_bytes(dtype));
-  const size_t smem = bins_bytes(pl.cluster);
+  const size_t smem = bins_bytes(pl.cluster, dtype_bytes(dtype));
   const long long grid = (long long)B * pl.cluster;
   if (dtype == EAGLE_F32)
     return launch_cluster(accept_sampling_kernel<float>, grid, pl.cluster, smem, pdl, s, static_cast<const float*>(tgt),
