@@ -47,7 +47,7 @@ typedef unsigned long long u64;
 constexpr int kSmpThreads = 256;
 constexpr int kSmpWarps = kSmpThreads / 32;
 constexpr int kSmpMaxCluster = 16;
-constexpr int kSmpBatch = 4;  // 16-byte loads a thread has in flight
+constexpr int kSmpBatch = 4;  // 16-byte loads a thread has in flight (passes that only count: twice as many)
 constexpr int kWeightBits = 44;
 constexpr int kListCap = 1024;  // fp32: tokens gathered around a cut
 
@@ -291,17 +291,17 @@ struct Team {
 };
 
 // f(vector, its index) over the CTA's slice, each(): f(logit, id).
-template <typename T, typename F>
+template <typename T, int BATCH = kSmpBatch, typename F>
 __device__ __forceinline__ void each_vec(const RowSlice<T>& sl, F&& f) {
-  for (int v0 = threadIdx.x; v0 < sl.nvec; v0 += kSmpThreads * kSmpBatch) {
-    uint4 u[kSmpBatch];
+  for (int v0 = threadIdx.x; v0 < sl.nvec; v0 += kSmpThreads * BATCH) {
+    uint4 u[BATCH];
 #pragma unroll
-    for (int i = 0; i < kSmpBatch; ++i) {
+    for (int i = 0; i < BATCH; ++i) {
       const int v = v0 + i * kSmpThreads;
       u[i] = v < sl.nvec ? sl.get(v) : Elem<T>::neg_inf_vec();
     }
 #pragma unroll
-    for (int i = 0; i < kSmpBatch; ++i) {
+    for (int i = 0; i < BATCH; ++i) {
       const int v = v0 + i * kSmpThreads;
       if (v >= sl.nvec) break;
       f(u[i], v);
@@ -337,17 +337,18 @@ __device__ __forceinline__ void select_local(SmpShared& sm, const RowSlice<T>& s
     for (int e = 0; e < E; ++e) s += g(y[e], sl.first + v * E + e);
     return s;
   };
+  constexpr int kBatch = 4;
   auto region_sum = [&](int v0, int count) {  // of the warp, count a multiple of 32
     u64 s = 0;
-    for (int i = 0; i < count; i += 32 * kSmpBatch) {
-      uint4 u[kSmpBatch];
+    for (int i = 0; i < count; i += 32 * kBatch) {
+      uint4 u[kBatch];
 #pragma unroll
-      for (int q = 0; q < kSmpBatch; ++q) {
+      for (int q = 0; q < kBatch; ++q) {
         const int v = v0 + i + q * 32 + lane;
         u[q] = v < sl.nvec && i + q * 32 < count ? sl.get(v) : Elem<T>::neg_inf_vec();
       }
 #pragma unroll
-      for (int q = 0; q < kSmpBatch; ++q) {
+      for (int q = 0; q < kBatch; ++q) {
         const int v = v0 + i + q * 32 + lane;
         if (v < sl.nvec && i + q * 32 < count) s += vec_sum(u[q], v);
       }
@@ -579,25 +580,40 @@ __device__ __forceinline__ u64 cta_exclusive(SmpShared& sm, u64 mine, u64* all) 
 }
 
 // The first bin (in descending order of value) at which the running measure of
-// the cluster reaches `need`; per bin `of(j)`, per CTA the measure `seg`
-// of its segment, this thread's part `mine` of it (bins [j0, j1)).  One
-// thread of the cluster calls found(bin, measure before it) if need is reached.
+// the cluster reaches `need`; per bin `of(j)`, per CTA the measure `seg` of its
+// segment, `mine` this thread's part of it.  A warp's bins are [j0, j1), its lanes
+// take them in turn.  One thread of the cluster calls found(bin, measure before
+// it) if need is reached.
 template <typename O, typename F>
 __device__ __forceinline__ void find_bin(Team& tm, const u64* seg, u64 need, u64 mine, int j0, int j1, O&& of,
                                          F&& found) {
   u64 before;
   if (owner_of(seg, tm.size, need - 1, before) != tm.rank) return;
-  u64 at = cta_exclusive(*tm.sm, mine, nullptr) + before;
-  int hit = -1;
-  u64 run = at;
-  if (need > at && need <= at + mine) {
-    for (int j = j0; j < j1 && hit < 0; ++j) {
-      const u64 m = of(j);
-      if (need <= run + m) hit = j;
-      else run += m;
-    }
+  SmpShared& sm = *tm.sm;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const u64 own = warp_sum_u64(mine);
+  __syncthreads();
+  if (lane == 0) sm.warp_part[0][warp] = own;
+  __syncthreads();
+  u64 at = before;
+#pragma unroll
+  for (int w = 0; w < kSmpWarps; ++w) {
+    const u64 y = sm.warp_part[0][w];
+    if (w < warp) at += y;
   }
-  if (hit >= 0) found(hit, run);
+  __syncthreads();
+  if (need <= at || need > at + own) return;  // the same in every lane
+  for (int j = j0 + lane; j - lane < j1; j += 32) {
+    const u64 m = j < j1 ? of(j) : 0;
+    if (!__any_sync(kFull, m != 0)) continue;
+    const u64 inc = warp_scan_u64(m);
+    const unsigned hit = __ballot_sync(kFull, need <= at + inc);
+    if (hit) {
+      if (lane == __ffs(hit) - 1) found(j, at + inc - m);
+      return;
+    }
+    at += __shfl_sync(kFull, inc, 31);
+  }
 }
 
 // Sort n <= kListCap keys of shared memory in descending order (whole CTA).
@@ -650,7 +666,7 @@ __device__ __forceinline__ bool cut_by_bins(Team& tm, const RowSlice<T>& sl, con
   __syncthreads();
   float m = -INFINITY;
   const uint32_t bins_at = (uint32_t)__cvta_generic_to_shared(tm.bins);
-  each_vec<T>(sl, [&](const uint4& u, int) {
+  each_vec<T, 2 * kSmpBatch>(sl, [&](const uint4& u, int) {
     const uint32_t word[4] = {u.x, u.y, u.z, u.w};
     if constexpr (kExact) {
       // two logits at a time: magnitudes clamped to the bins' range, their
@@ -684,22 +700,29 @@ __device__ __forceinline__ bool cut_by_bins(Team& tm, const RowSlice<T>& sl, con
   cluster_sync();
   // ---- this CTA's segment of the bins, summed over the cluster
   const int seg = (kBins + tm.size - 1) / tm.size, seg0 = tm.rank * seg, seg1 = min(kBins, seg0 + seg);
-  const int bpt = ((seg + kSmpThreads - 1) / kSmpThreads) | 1;  // odd: threads' bins lie in different banks
-  const int j0 = min(seg1, seg0 + tid * bpt), j1 = min(seg1, j0 + bpt);
+  // (a warp takes neighbouring bins, 32 at a time: the values that occur lie close together)
+  const int lane = tid & 31, warp = tid >> 5;
+  const int per_warp = (seg + 32 * kSmpWarps - 1) / (32 * kSmpWarps) * 32;
+  const int j0 = min(seg1, seg0 + warp * per_warp), j1 = min(seg1, j0 + per_warp);
   u64 first = 0;  // order bits of the largest value counted
-  for (int j = j0; j < j1; ++j) {
+  for (int j = j0 + lane; j < j1; j += 32) {
     uint32_t c = 0;
     const int at = slot_of(j);
     if (tm.size == 1) {
       c = tm.bins[at];
     } else {
-#pragma unroll 4
-      for (int r = 0; r < tm.size; ++r) c += remote_load32(remote(tm.bins + at, r));
+      uint32_t part[kSmpMaxCluster];
+#pragma unroll
+      for (int r = 0; r < kSmpMaxCluster; ++r) part[r] = r < tm.size ? remote_load32(remote(tm.bins + at, r)) : 0;
+#pragma unroll
+      for (int r = 0; r < kSmpMaxCluster; ++r) c += part[r];
       tm.sums[j - seg0] = c;
       if (placed && c && j < kZeroBin) {
         uint32_t l = 0;
-#pragma unroll 4
-        for (int r = 0; r < tm.size; ++r) l += remote_load32(remote(tm.lows + at, r));
+#pragma unroll
+        for (int r = 0; r < kSmpMaxCluster; ++r) part[r] = r < tm.size ? remote_load32(remote(tm.lows + at, r)) : 0;
+#pragma unroll
+        for (int r = 0; r < kSmpMaxCluster; ++r) l += part[r];
         tm.lows[kNegative + j - seg0] = l;
       }
     }
@@ -734,7 +757,7 @@ __device__ __forceinline__ bool cut_by_bins(Team& tm, const RowSlice<T>& sl, con
     auto mass_of = [&](int j, uint32_t c) { return c && j < kLastBin ? c * weight(s, sm.tab, bin_value(j, 0)) : 0ull; };
     auto count_of = [&](int j, uint32_t c) { return j < kLastBin ? (u64)c : 0ull; };
     u64 n = 0, w = 0;
-    for (int j = j0; j < j1; ++j) {
+    for (int j = j0 + lane; j < j1; j += 32) {
       const uint32_t c = sum_at(j);
       n += count_of(j, c);
       if (ask.by_p) w += mass_of(j, c);
@@ -760,7 +783,7 @@ __device__ __forceinline__ bool cut_by_bins(Team& tm, const RowSlice<T>& sl, con
         if (ask.by_p) {
           // Z: the weight above the bin, and the ties'
           u64 above = 0, unused = 0;
-          for (int j = j0; j < min(j1, cut_bin); ++j) above += mass_of(j, sum_at(j));
+          for (int j = j0 + lane; j < min(j1, cut_bin); j += 32) above += mass_of(j, sum_at(j));
           tm.sums2(above, unused);
           Z = above + ties * weight(s, sm.tab, bin_value(cut_bin, 0));
         }
@@ -860,7 +883,7 @@ __device__ __forceinline__ bool cut_by_bins(Team& tm, const RowSlice<T>& sl, con
       return (u64)((double)c * (double)w1 * (c > 1 ? 1.0 + (double)fminf(wide * wide, 1.f) / 24.0 : 1.0));
     };
     u64 n = 0, w = 0;
-    for (int j = j0; j < j1; ++j) {
+    for (int j = j0 + lane; j < j1; j += 32) {
       const uint32_t c = sum_at(j);
       n += count_of(j, c);
       if (ask.by_p) w += guess_of(j, c);
@@ -895,7 +918,7 @@ __device__ __forceinline__ bool cut_by_bins(Team& tm, const RowSlice<T>& sl, con
         hi_bin = (int)tm.heard()[0];
         // few tokens up to there: list them all, so that nothing depends on the estimate's lower end
         u64 upto = 0, unused = 0;
-        for (int j = j0; j < min(j1, hi_bin + 1); ++j) upto += sum_at(j);
+        for (int j = j0 + lane; j < min(j1, hi_bin + 1); j += 32) upto += sum_at(j);
         tm.sums2(upto, unused);
         if (upto <= (u64)kListCap) lo_bin = 0;
       }
@@ -907,11 +930,13 @@ __device__ __forceinline__ bool cut_by_bins(Team& tm, const RowSlice<T>& sl, con
     // above: tokens before the listed bins; Z: all
     u64 Z = 0, above = 0, kept_above = 0;
     const uint32_t list_n = remote(&sm.list_n, 0), list = remote(sm.list, 0);  // CTA 0's
+    // the listed bins as values: from the least of hi_bin to the largest of lo_bin
+    const float list_lo = !listed ? INFINITY : (hi_bin < kZeroBin ? bin_value(hi_bin, 0) : (hi_bin == kZeroBin ? -0x1p-16f : bin_value(hi_bin, 0xffffu)));
+    const float list_hi = !listed ? -INFINITY : (lo_bin < kZeroBin ? bin_value(lo_bin, 0xffffu) : (lo_bin == kZeroBin ? 0x1p-16f : bin_value(lo_bin, 0)));
     each<T>(sl, [&](float x, int id) {
-      const int j = bin_of(__float_as_uint(x) >> 16);
-      const bool in = listed && j >= lo_bin && j <= hi_bin && x > -INFINITY;
-      const bool before = !listed || j < lo_bin;
-      if ((window || before) && x == x) {
+      const bool before = x > list_hi;
+      const bool in = x >= list_lo && !before;
+      if (window || before) {
         const u64 y = weight(s, sm.tab, x);
         Z += y;
         if (before) above += y;
@@ -1108,7 +1133,7 @@ __device__ __forceinline__ void draw_kept(Team& tm, RowSlice<T> sl, RowStat s, d
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kSmpThreads, 2)
+__global__ void __launch_bounds__(kSmpThreads, 4)
 sample_kernel(const T* __restrict__ logits, int V, long long stride, eagle_sampling_t params,
               const float* __restrict__ uniforms, int32_t* __restrict__ tokens, float* __restrict__ logprob, int per) {
   __shared__ SmpShared sm;
