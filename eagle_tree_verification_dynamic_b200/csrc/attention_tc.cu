@@ -48,6 +48,7 @@ namespace eagle {
 using namespace sm100;
 
 constexpr int kTcThreads = 320;   // 10 warps: producer, MMA, 8 softmax
+constexpr int kWideThreads = 352;  // wide tiles: a second MMA warp (the last)
 constexpr int kBN = kAttnKeysPerTile;
 constexpr int kRowsPerCta = kAttnRowsPerUnit;
 constexpr int kMaxStages = 12;
@@ -57,7 +58,14 @@ constexpr int kCombineThreads = 128;
 // Shared memory from the (1024-byte aligned) dynamic base: a 3 KB header
 // (barriers, then each row's (max, sum) exchange between the two softmax
 // warps of a lane quarter), two Q buffers, the K/V ring (P lives in TMEM).
-template <int D>
+// WIDE: how the two softmax warps of a lane quarter share the tiles.  Narrow: each
+// tile's keys in halves (32 per thread), three S buffers; the shortest way from
+// a tile to its product, for CTAs with a handful of tiles.  Wide: whole tiles in
+// turn (64 keys per thread), four S buffers, O_A over a piece's even tiles and
+// O_B over its odd ones: the waits, the TMEM round trips and the reductions of a
+// tile come once per 64 keys and overlap the other warps' tile, for CTAs that
+// stream many tiles.
+template <int D, bool WIDE = false>
 struct TcLayout {
   static constexpr int kAtoms = D / 64;               // 128-byte column atoms along D
   static constexpr int kQBytes = kAtoms * 128 * 128;  // 128 rows
@@ -80,7 +88,7 @@ struct TcLayout {
   // at the buffer's columns 0..15, keys 32..63 at columns 32..47, each inside
   // the columns of S its own warp has already read.
   static constexpr uint32_t kTmemCols = 512;
-  static constexpr int kSBufs = 3;
+  static constexpr int kSBufs = WIDE ? 4 : 3;
   static constexpr uint32_t kColS = 0;  // S buffer i at column 64 * i
   static constexpr uint32_t kColOA = kSBufs * 64;
   static constexpr uint32_t kColOB = kSBufs * 64 + D;
@@ -95,10 +103,11 @@ struct TcBars {
   uint64_t q_empty[2];
   uint64_t full[kMaxStages];
   uint64_t empty[kMaxStages];
-  uint64_t s_full[3];
-  uint64_t p_full[3][2];  // per S buffer, per half of the tile's keys (the four warps writing that half)
-  uint64_t pv_done[3];
+  uint64_t s_full[4];
+  uint64_t p_full[4][2];  // per S buffer, per half of the tile's keys (the four warps writing that half; wide: [0])
+  uint64_t pv_done[4];
   uint64_t mma_idle;
+  uint64_t s_idle;   // wide: the S warp's
   uint64_t pair[4];  // per lane quarter: both softmax warps wrote their (max, sum)
   uint64_t never;    // nothing arrives here: the wait probe's barrier
   uint32_t tmem_base;
@@ -241,6 +250,7 @@ __device__ __forceinline__ void geom_locate(const AttnGeom& a, long long t, int 
 
 // CTA c holds tiles [c*T/C, (c+1)*T/C); this is the CTA holding tile t.
 __device__ __forceinline__ int cta_of_tile(long long t, long long T, int C) {
+  if (T * C < 0xffffffffLL) return (int)(((uint32_t)(t + 1) * (uint32_t)C - 1u) / (uint32_t)T);
   return (int)(((t + 1) * C - 1) / T);
 }
 // With fewer tiles than CTAs (a ragged batch far below Lmax) some ranges are empty.
@@ -390,11 +400,10 @@ __device__ __forceinline__ int table_entry(const int32_t* bt, int idx, int width
 // (kModeSinks only reports pages that hold a key some row sees: a page between
 // the sinks and the window may have been given back.)
 // Returns false when a wait gave up.
-template <int D, int MODE>
+template <int D, int MODE, typename Lay = TcLayout<D>>
 __device__ bool produce_paged(const TcParams& p, const AttnGeom& a, const Piece& pc, int g, uint32_t s_base,
                               TcBars* bars, volatile int* abort, const CUtensorMap* tm_k, const CUtensorMap* tm_v,
                               const CUtensorMap* tm_kt, const CUtensorMap* tm_vt, int lane, int& jg) {
-  using Lay = TcLayout<D>;
   constexpr int S = Lay::kStages;
   const int ps = p.page_size;
   const int sub = ps < kBN ? ps : kBN;  // keys per box
@@ -465,20 +474,123 @@ __device__ __forceinline__ uint32_t low_bits(int count) {
   return count >= 32 ? 0xffffffffu : (count > 0 ? (1u << count) - 1u : 0u);
 }
 
+// A batch over a shared prefix is bound by arithmetic, with about a hundred tiles
+// and more a CTA: wide (32 sequences over 4096 shared keys 205 -> @@ us, 16 over
+// 32763, 80-node trees, 1740 -> @@ us).
+template <int MODE>
+constexpr bool kWideTiles = MODE == kModeShared;
+
 // How long a waiting softmax warp or producer lane may sleep per poll (ns):
 // the MMA warp shares a scheduler with two softmax warps, and a warp that
 // polls in a tight loop takes issue slots from it.
 constexpr uint32_t kSoftmaxSleepNs = 300u;
 constexpr uint32_t kProducerSleepNs = 500u;
 
+// The MMA warps over wide tiles: one issues S = Q K^T, the other O += P V.  Each
+// goes through its schedule with all lanes and only the issue itself is one
+// lane's, so that addresses and descriptors stay in uniform registers, where the
+// instruction wants them.  A tile costs such a warp some 500 cycles of waits,
+// elections and commits, as much as the tensor pipe needs for it, so one warp
+// doing both was the bound (with no MMA, no softmax and no load at all the tiles
+// still took 0.55 us each).  S(j) goes where P(j - NB) was, once its PV is done.
 template <int D, int MODE>
-__global__ void __launch_bounds__(kTcThreads, 1)
+__device__ __forceinline__ void mma_scores(const AttnGeom& a, TcBars* bars, uint32_t s_base, uint32_t tmem,
+                                           volatile int* abort) {
+  using Lay = TcLayout<D, true>;
+  constexpr int S = Lay::kStages, NB = Lay::kSBufs;
+  constexpr uint32_t id_qk = idesc_bf16_f32(128, kBN, 0, 0);
+  const int total = __shfl_sync(kFull, bars->n_tiles, 0);
+  const uint64_t q_desc = smem_desc(s_base + Lay::kQOff, 16, 1024, kSwizzle128B);
+  const uint64_t k_desc = smem_desc(s_base + Lay::kStageOff, 16, 1024, kSwizzle128B);
+  PieceCursor<MODE> cur;
+  cur.init(bars);
+  Piece pc;
+  int si = -1, rem = 0, st = 0, ph = 0;  // piece, tiles left in it, stage and its parity
+  for (int j = 0; j < total; ++j) {
+    if (rem == 0) {
+      cur.next(a, pc);
+      ++si;
+      rem = __shfl_sync(kFull, pc.te - pc.tb, 0);
+      if (!__all_sync(kFull, mbar_wait(smem_u32(&bars->q_full[si & 1]), (si >> 1) & 1, abort))) break;
+    }
+    --rem;
+    const int jb = j - NB;
+    if (jb >= 0 && !__all_sync(kFull, mbar_wait(smem_u32(&bars->pv_done[j % NB]), (uint32_t)(jb / NB) & 1u, abort))) break;
+    if (!__all_sync(kFull, mbar_wait(smem_u32(&bars->full[st]), ph, abort))) break;
+    tc_fence_after();
+    const uint64_t da = q_desc + (uint64_t)((si & 1) * (Lay::kQBytes >> 4));
+    const uint64_t db = k_desc + (uint64_t)(st * (Lay::kStageBytes >> 4));
+    const uint32_t t_s = tmem + Lay::kColS + (uint32_t)((j % NB) * kBN);
+    if (elect_one()) {
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk)
+        mma_bf16_ss(t_s, da + ((kk / 4) * 16384 + (kk % 4) * 32) / 16,
+                    db + ((kk / 4) * Lay::kKVAtomBytes + (kk % 4) * 32) / 16, id_qk, kk > 0);
+      mma_commit(smem_u32(&bars->s_full[j % NB]));
+      if (rem == 0) mma_commit(smem_u32(&bars->q_empty[si & 1]));
+    }
+    __syncwarp();
+    if (++st == S) {
+      st = 0;
+      ph ^= 1;
+    }
+  }
+  // every MMA has finished before TMEM is released
+  if (elect_one()) mma_commit(smem_u32(&bars->s_idle));
+  __syncwarp();
+  mbar_wait_drain(smem_u32(&bars->s_idle), 0, 200000000ull);
+}
+
+template <int D, int MODE>
+__device__ __forceinline__ void mma_outputs(const AttnGeom& a, TcBars* bars, uint32_t s_base, uint32_t tmem,
+                                            volatile int* abort) {
+  using Lay = TcLayout<D, true>;
+  constexpr int S = Lay::kStages, NB = Lay::kSBufs;
+  constexpr uint32_t id_pv = idesc_bf16_f32(128, D, 0, 1);
+  const int total = __shfl_sync(kFull, bars->n_tiles, 0);
+  const uint64_t v_desc = smem_desc(s_base + Lay::kStageOff + Lay::kKBytes, Lay::kKVAtomBytes, 1024, kSwizzle128B);
+  PieceCursor<MODE> cur;
+  cur.init(bars);
+  Piece pc;
+  int rem = 0, tix = 0, st = 0;  // tiles left in the piece, tile of the piece, stage
+  for (int j = 0; j < total; ++j, ++tix) {
+    if (rem == 0) {
+      cur.next(a, pc);
+      rem = __shfl_sync(kFull, pc.te - pc.tb, 0);
+      tix = 0;
+    }
+    --rem;
+    // (P(j) is there, so S(j) and with it this stage's copies have landed)
+    if (!__all_sync(kFull, mbar_wait(smem_u32(&bars->p_full[j % NB][0]), (uint32_t)(j / NB) & 1u, abort))) break;
+    tc_fence_after();
+    const uint64_t db = v_desc + (uint64_t)(st * (Lay::kStageBytes >> 4));
+    const uint32_t t_p = tmem + Lay::kColS + (uint32_t)((j % NB) * kBN);
+    const uint32_t t_o = tmem + ((tix & 1) ? Lay::kColOB : Lay::kColOA);
+    const uint32_t more = tix >= 2 ? 1u : 0u;  // an accumulator starts at the piece's first even, first odd tile
+    if (elect_one()) {
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk) mma_bf16_ts(t_o, t_p + (uint32_t)(kk * 8), db + kk * 2048 / 16, id_pv, kk ? 1u : more);
+      mma_commit(smem_u32(&bars->empty[st]));
+      mma_commit(smem_u32(&bars->pv_done[j % NB]));
+    }
+    __syncwarp();
+    if (++st == S) st = 0;
+  }
+  if (elect_one()) mma_commit(smem_u32(&bars->mma_idle));
+  __syncwarp();
+  mbar_wait_drain(smem_u32(&bars->mma_idle), 0, 200000000ull);
+}
+
+template <int D, int MODE>
+__global__ void __launch_bounds__(kWideTiles<MODE> ? kWideThreads : kTcThreads, 1)
 attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                const __grid_constant__ CUtensorMap tm_kt, const __grid_constant__ CUtensorMap tm_vt,
                const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_ks,
                const __grid_constant__ CUtensorMap tm_vs, const TcParams p) {
-  using Lay = TcLayout<D>;
+  constexpr bool kWide = kWideTiles<MODE>;
+  using Lay = TcLayout<D, kWide>;
   constexpr int S = Lay::kStages;
+  constexpr int NB = Lay::kSBufs;
   extern __shared__ __align__(1024) unsigned char smem[];
   const AttnGeom& a = p.geo;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -502,12 +614,12 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
       mbar_init(smem_u32(&bars->q_full[i]), 1);
       mbar_init(smem_u32(&bars->q_empty[i]), 1);
     }
-    for (int i = 0; i < 3; ++i) {
+    for (int i = 0; i < NB; ++i) {
       mbar_init(smem_u32(&bars->s_full[i]), 1);
       // every softmax thread of a half (4 warps) arrives for every tile, rows
-      // or not; S(j) is written only after PV(j - 3) was issued, so a phase
+      // or not; S(j) is written only after PV(j - NB) was issued, so a phase
       // completes before the next one on the same barrier begins
-      mbar_init(smem_u32(&bars->p_full[i][0]), 128);
+      mbar_init(smem_u32(&bars->p_full[i][0]), kWide ? 4 : 128);  // (wide: one arrival per warp)
       mbar_init(smem_u32(&bars->p_full[i][1]), 128);
       mbar_init(smem_u32(&bars->pv_done[i]), 1);
     }
@@ -516,6 +628,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
       mbar_init(smem_u32(&bars->empty[i]), 1);
     }
     mbar_init(smem_u32(&bars->mma_idle), 1);
+    mbar_init(smem_u32(&bars->s_idle), 1);
     for (int i = 0; i < 4; ++i) mbar_init(smem_u32(&bars->pair[i]), 64);
     mbar_init(smem_u32(&bars->never), 1);
     bars->abort = 0;
@@ -557,7 +670,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
       bars->hr0 = hr0;
       bars->off0 = off0;
     }
-    if (warp >= 2) {
+    if (warp >= 2 && warp < kTcThreads / 32) {
       scur.init(b0, hr0, off0, (int)(t1 - t0));
       s_have = scur.next(a, spc);
       // issued before the block barrier, so ahead of the first K/V copies,
@@ -692,7 +805,9 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
       griddep_wait();
       griddep_launch_dependents();
     }
-    if (lane == 0) {
+    if constexpr (kWide) {
+      mma_scores<D, MODE>(a, bars, __shfl_sync(kFull, s_base, 0), __shfl_sync(kFull, tmem, 0), abort);
+    } else if (lane == 0) {
       const uint32_t id_qk = idesc_bf16_f32(128, kBN, 0, 0);
       const uint32_t id_pv = idesc_bf16_f32(128, D, 0, 1);
       const uint32_t t_oa = tmem + Lay::kColOA, t_ob = tmem + Lay::kColOB;
@@ -722,15 +837,15 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
         // issue whatever is ready: the next QK^T (its Q and K landed; at most
         // two tiles ahead), and this tile's PV per half of its keys (that
         // half's P is written)
-        const int pbuf = jp % 3;
-        const uint32_t ppar = (uint32_t)(jp / 3) & 1u;
+        const int pbuf = jp % NB;
+        const uint32_t ppar = (uint32_t)(jp / NB) & 1u;
         const int st = jp % S;
         const uint32_t p_tmem = tmem + Lay::kColS + (uint32_t)(pbuf * kBN);
         const uint32_t v_addr = s_base + Lay::kStageOff + st * Lay::kStageBytes + Lay::kKBytes;
         bool done_h[2] = {false, false};
         uint64_t tw = 0;
         for (uint32_t it = 0;; ++it) {
-          if (jq < total && jq <= jp + 2) {
+          if (jq < total && jq <= jp + NB - 1) {
             if (q_rem == 0) {
               qc.next(a, qp);
               ++q_si;
@@ -742,7 +857,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
               tc_fence_after();
               const uint32_t q_addr = s_base + Lay::kQOff + qb * Lay::kQBytes;
               const uint32_t k_addr = s_base + Lay::kStageOff + (jq % S) * Lay::kStageBytes;
-              const uint32_t t_s = tmem + Lay::kColS + (uint32_t)((jq % 3) * kBN);
+              const uint32_t t_s = tmem + Lay::kColS + (uint32_t)((jq % NB) * kBN);
 #pragma unroll
               for (int kk = 0; kk < D / 16; ++kk) {
                 const uint32_t off = (kk % 4) * 32;
@@ -750,7 +865,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
                 const uint64_t db = smem_desc(k_addr + (kk / 4) * Lay::kKVAtomBytes + off, 16, 1024, kSwizzle128B);
                 mma_bf16_ss(t_s, da, db, id_qk, kk > 0);
               }
-              mma_commit(smem_u32(&bars->s_full[jq % 3]));
+              mma_commit(smem_u32(&bars->s_full[jq % NB]));
               if (--q_rem == 0) mma_commit(smem_u32(&bars->q_empty[qb]));
               ++jq;
             }
@@ -792,6 +907,12 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
       mma_commit(smem_u32(&bars->mma_idle));
       mbar_wait_drain(smem_u32(&bars->mma_idle), 0, 200000000ull);
     }
+  } else if (kWide && warp == kWideThreads / 32 - 1) {
+    if (p.early) {
+      griddep_wait();
+      griddep_launch_dependents();
+    }
+    mma_outputs<D, MODE>(a, bars, __shfl_sync(kFull, s_base, 0), __shfl_sync(kFull, tmem, 0), abort);
   } else {
     // ------------------------------------------------------------- softmax
     // warps 2..9: quad = TMEM lane quarter (32 query rows); half = which 32
@@ -800,7 +921,8 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
     // per piece.
     const int half = (warp - 2) >> 2;
     const uint32_t lane_base = (uint32_t)(quad * 32) << 16;
-    const uint32_t t_s = tmem + lane_base + Lay::kColS + (uint32_t)(half * 32);
+    constexpr int KW = kWide ? 64 : 32;  // keys per thread and tile
+    const uint32_t t_s = tmem + lane_base + Lay::kColS + (uint32_t)(kWide ? 0 : half * 32);
     const uint32_t t_own = tmem + lane_base + (half ? Lay::kColOB : Lay::kColOA);
     const uint32_t t_oa = tmem + lane_base + Lay::kColOA, t_ob = tmem + lane_base + Lay::kColOB;
     float2* xch = reinterpret_cast<float2*>(smem + Lay::kXchOff);  // [half][row]
@@ -835,8 +957,9 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
       const int win_lo = rc.qpos - a.window + 1;
       float m_used = -INFINITY, l = 0.f;  // reference max (scaled, log2) and row sum of this half
       for (int t = pc.tb; t < pc.te; ++t, ++jg) {
-        const int sbuf = jg % 3;
-        if (!__all_sync(kFull, mbar_wait(smem_u32(&bars->s_full[sbuf]), (uint32_t)(jg / 3) & 1u, abort, 2000000000ull,
+        if (kWide && ((t - pc.tb) & 1) != half) continue;  // the other four warps' tile
+        const int sbuf = jg % NB;
+        if (!__all_sync(kFull, mbar_wait(smem_u32(&bars->s_full[sbuf]), (uint32_t)(jg / NB) & 1u, abort, 2000000000ull,
                                          kSoftmaxSleepNs))) {
           ok = false;
           break;
@@ -847,73 +970,87 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
           // 0 x NaN is NaN: this half's such rows of V are zeroed before P says
           // that PV may read them.  Only a range's first or last tile has any.
           const bool tree = t >= pc.ptiles;
-          const int key0 = (tree ? (t - pc.ptiles) * kBN : piece_key0<MODE>(pc, t)) + half * 32;
-          uint32_t seen = low_bits((tree ? a.n : pc.L) - key0);
-          if (MODE == kModeSinks && !tree) seen &= ~low_bits(pc.L - a.window + 1 - key0) | low_bits(a.sinks - key0);
-          if (seen != 0xffffffffu) {  // the same in every warp of the half
-            unsigned char* v = smem + Lay::kStageOff + (jg % S) * Lay::kStageBytes + Lay::kKBytes + half * 32 * 128;
-            for (int e = r_local; e < 32 * Lay::kAtoms * 8; e += 128) {
-              const int key = e / (Lay::kAtoms * 8), piece = e % (Lay::kAtoms * 8);
-              if (!((seen >> key) & 1u))
-                *reinterpret_cast<uint4*>(v + (piece / 8) * Lay::kKVAtomBytes + key * 128 + (piece % 8) * 16) =
-                    make_uint4(0, 0, 0, 0);
+          const int key0 = (tree ? (t - pc.ptiles) * kBN : piece_key0<MODE>(pc, t)) + (kWide ? 0 : half * 32);
+#pragma unroll
+          for (int hh = 0; hh < KW / 32; ++hh) {
+            const int k0 = key0 + hh * 32;
+            uint32_t seen = low_bits((tree ? a.n : pc.L) - k0);
+            if (MODE == kModeSinks && !tree) seen &= ~low_bits(pc.L - a.window + 1 - k0) | low_bits(a.sinks - k0);
+            if (seen != 0xffffffffu) {  // the same in every warp of the half
+              unsigned char* v = smem + Lay::kStageOff + (jg % S) * Lay::kStageBytes + Lay::kKBytes +
+                                 (kWide ? hh : half) * 32 * 128;
+              for (int e = r_local; e < 32 * Lay::kAtoms * 8; e += 128) {
+                const int key = e / (Lay::kAtoms * 8), piece = e % (Lay::kAtoms * 8);
+                if (!((seen >> key) & 1u))
+                  *reinterpret_cast<uint4*>(v + (piece / 8) * Lay::kKVAtomBytes + key * 128 + (piece % 8) * 16) =
+                      make_uint4(0, 0, 0, 0);
+              }
+              fence_proxy_async_smem();
             }
-            fence_proxy_async_smem();
           }
         }
         if (warp_live) {
           tc_fence_after();
-          float x[32];
-          tmem_ld32(t_s + (uint32_t)(sbuf * kBN), x);
+          float x[KW];
+#pragma unroll
+          for (int hh = 0; hh < KW / 32; ++hh)
+            tmem_ld32(t_s + (uint32_t)(sbuf * kBN + hh * 32), x + hh * 32);
           tmem_wait_ld();
           const bool tree = t >= pc.ptiles;
-          const int key0 = (tree ? (t - pc.ptiles) * kBN : piece_key0<MODE>(pc, t)) + half * 32;
-          const int k1 = tree ? a.n : pc.L;
-          // visibility of this half's 32 keys as one bit mask, built the same
-          // way on every tile (so the code stays hot in the instruction cache):
-          // keys below the piece's end, then the ancestor bits (tree keys) or
-          // the window's lower bound (prefix keys)
-          const int lim = k1 - key0;
-          uint32_t vm = low_bits(lim);
-          const uint64_t mw = key0 >= 64 ? rc.mw1 : rc.mw0;
-          const uint32_t tree_bits = (uint32_t)(mw >> (key0 & 63));
-          const int lo_cut = win_lo - key0;  // prefix keys below it are outside the window
-          uint32_t win_bits =
-              (MODE == kModeShared || a.window == 0 || lo_cut <= 0) ? 0xffffffffu : (lo_cut >= 32 ? 0u : ~((1u << lo_cut) - 1u));
-          if (MODE == kModeSinks) win_bits |= low_bits(a.sinks - key0);
-          vm &= tree ? tree_bits : win_bits;
-          if (!row_ok) vm = 0u;
-          if (MODE != kModeShared && tree && a.window > 0) {  // the window on tree keys' positions (rare; warp-uniform)
-            const int grp = key0 >> 5;
-            const int tsel = grp == 0 ? rc.tpos[0] : grp == 1 ? rc.tpos[1] : grp == 2 ? rc.tpos[2] : rc.tpos[3];
+          float mx = -INFINITY;
 #pragma unroll
-            for (int cc = 0; cc < 32; ++cc) {
-              const int kpos = __shfl_sync(kFull, tsel, cc);  // every lane takes part
-              if (kpos < win_lo && !(MODE == kModeSinks && kpos < a.sinks)) vm &= ~(1u << cc);
+          for (int hh = 0; hh < KW / 32; ++hh) {
+            float* xh = x + hh * 32;
+            const int key0 = (tree ? (t - pc.ptiles) * kBN : piece_key0<MODE>(pc, t)) + (kWide ? hh : half) * 32;
+            const int k1 = tree ? a.n : pc.L;
+            // visibility of 32 keys as one bit mask, built the same way on every
+            // tile (so the code stays hot in the instruction cache): keys below
+            // the piece's end, then the ancestor bits (tree keys) or the window's
+            // lower bound (prefix keys)
+            const int lim = k1 - key0;
+            uint32_t vm = low_bits(lim);
+            const uint64_t mw = key0 >= 64 ? rc.mw1 : rc.mw0;
+            const uint32_t tree_bits = (uint32_t)(mw >> (key0 & 63));
+            const int lo_cut = win_lo - key0;  // prefix keys below it are outside the window
+            uint32_t win_bits =
+                (MODE == kModeShared || a.window == 0 || lo_cut <= 0) ? 0xffffffffu : (lo_cut >= 32 ? 0u : ~((1u << lo_cut) - 1u));
+            if (MODE == kModeSinks) win_bits |= low_bits(a.sinks - key0);
+            vm &= tree ? tree_bits : win_bits;
+            if (!row_ok) vm = 0u;
+            if (MODE != kModeShared && tree && a.window > 0) {  // the window on tree keys' positions (rare; warp-uniform)
+              const int grp = key0 >> 5;
+              const int tsel = grp == 0 ? rc.tpos[0] : grp == 1 ? rc.tpos[1] : grp == 2 ? rc.tpos[2] : rc.tpos[3];
+#pragma unroll
+              for (int cc = 0; cc < 32; ++cc) {
+                const int kpos = __shfl_sync(kFull, tsel, cc);  // every lane takes part
+                if (kpos < win_lo && !(MODE == kModeSinks && kpos < a.sinks)) vm &= ~(1u << cc);
+              }
             }
-          }
-          if (__any_sync(kFull, vm != 0xffffffffu)) {  // most prefix tiles see every key
+            if (__any_sync(kFull, vm != 0xffffffffu)) {  // most prefix tiles see every key
 #pragma unroll
-            for (int cc = 0; cc < 32; ++cc) x[cc] = ((vm >> cc) & 1u) ? x[cc] : -INFINITY;
-          }
-          float m4[4] = {fmax3(x[0], x[1], x[2]), fmax3(x[3], x[4], x[5]), fmax3(x[6], x[7], x[8]),
-                         fmax3(x[9], x[10], x[11])};
+              for (int cc = 0; cc < 32; ++cc) xh[cc] = ((vm >> cc) & 1u) ? xh[cc] : -INFINITY;
+            }
+            float m4[4] = {fmax3(xh[0], xh[1], xh[2]), fmax3(xh[3], xh[4], xh[5]), fmax3(xh[6], xh[7], xh[8]),
+                           fmax3(xh[9], xh[10], xh[11])};
 #pragma unroll
-          for (int cc = 12; cc < 28; cc += 8) {
-            m4[0] = fmax3(m4[0], x[cc], x[cc + 1]);
-            m4[1] = fmax3(m4[1], x[cc + 2], x[cc + 3]);
-            m4[2] = fmax3(m4[2], x[cc + 4], x[cc + 5]);
-            m4[3] = fmax3(m4[3], x[cc + 6], x[cc + 7]);
+            for (int cc = 12; cc < 28; cc += 8) {
+              m4[0] = fmax3(m4[0], xh[cc], xh[cc + 1]);
+              m4[1] = fmax3(m4[1], xh[cc + 2], xh[cc + 3]);
+              m4[2] = fmax3(m4[2], xh[cc + 4], xh[cc + 5]);
+              m4[3] = fmax3(m4[3], xh[cc + 6], xh[cc + 7]);
+            }
+            const float mh = fmax3(fmax3(m4[0], m4[1], m4[2]), fmax3(m4[3], xh[28], xh[29]), fmaxf(xh[30], xh[31]));
+            mx = hh ? fmaxf(mx, mh) : mh;
           }
-          float mx = fmax3(fmax3(m4[0], m4[1], m4[2]), fmax3(m4[3], x[28], x[29]), fmaxf(x[30], x[31]));
           mx *= sl2;  // scale > 0 keeps the order
-          // (P of this tile replaces S(jg) in TMEM: PV(jg - 2), the last reader of
+          // (P of this tile replaces S(jg) in TMEM: PV(jg - NB), the last reader of
           // those columns, completed before QK^T(jg), whose commit s_full waited on)
           const bool rebase = mx > m_used + 8.f;
           if (__any_sync(kFull, rebase && t > pc.tb && l > 0.f)) {
-            // this half's O may only be rescaled once PV(jg - 1) has finished accumulating
-            if (!__all_sync(kFull, mbar_wait(smem_u32(&bars->pv_done[(jg - 1) % 3]), (uint32_t)((jg - 1) / 3) & 1u,
-                                             abort))) {
+            // these warps' O may only be rescaled once the PV before has finished
+            // accumulating into it (wide: that of two tiles ago)
+            const int jb = jg - (kWide ? 2 : 1);
+            if (!__all_sync(kFull, mbar_wait(smem_u32(&bars->pv_done[jb % NB]), (uint32_t)(jb / NB) & 1u, abort))) {
               ok = false;
               break;
             }
@@ -933,10 +1070,10 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
           if (rebase) m_used = mx;
           const float neg_m = m_used > -INFINITY ? -m_used : 0.f;  // no visible key yet: every x is -inf
           float2 s2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-          uint32_t packed[16];
+          uint32_t packed[KW / 2];
           const float2 sl2x2 = make_float2(sl2, sl2), nm2 = make_float2(neg_m, neg_m);
 #pragma unroll
-          for (int c2 = 0; c2 < 16; ++c2) {
+          for (int c2 = 0; c2 < KW / 2; ++c2) {
             const float2 z = ffma2(make_float2(x[2 * c2], x[2 * c2 + 1]), sl2x2, nm2);
             const float2 e = make_float2(ex2(z.x), ex2(z.y));
             s2[c2 & 1] = fadd2(s2[c2 & 1], e);
@@ -945,11 +1082,19 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
           }
           const float2 st2 = fadd2(s2[0], s2[1]);
           l += st2.x + st2.y;
-          tmem_st16u(t_s + (uint32_t)(sbuf * kBN), packed);  // P over this half's first 16 S columns
+          // P over the first columns of the S it came from (two keys per column)
+#pragma unroll
+          for (int hh = 0; hh < KW / 32; ++hh)
+            tmem_st16u(t_s + (uint32_t)(sbuf * kBN + hh * 16), packed + hh * 16);
           tmem_wait_st();
         }
         tc_fence_before();
-        mbar_arrive(smem_u32(&bars->p_full[sbuf][half]));
+        if constexpr (kWide) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&bars->p_full[sbuf][0]));
+        } else {
+          mbar_arrive(smem_u32(&bars->p_full[sbuf][half]));
+        }
       }
       if (!ok) break;
       // ---- end of the piece: merge the two halves' (max, sum), normalise,
@@ -957,7 +1102,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
       // writes its half of the output columns from both accumulators.
       if (warp_live) {
         const int jl = jg - 1;
-        if (!__all_sync(kFull, mbar_wait(smem_u32(&bars->pv_done[jl % 3]), (uint32_t)(jl / 3) & 1u, abort))) {
+        if (!__all_sync(kFull, mbar_wait(smem_u32(&bars->pv_done[jl % NB]), (uint32_t)(jl / NB) & 1u, abort))) {
           ok = false;
           break;
         }
@@ -986,7 +1131,11 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
           tmem_wait_ld();
           if (!row_ok) continue;
 #pragma unroll
-          for (int u = 0; u < 16; ++u) oa[u] = fmaf(oa[u], fa, ob[u] * fb);
+          for (int u = 0; u < 16; ++u) {
+            // (wide: a piece of one tile never wrote O_B)
+            if (kWide) oa[u] = fmaf(oa[u], fa, fb > 0.f ? ob[u] * fb : 0.f);
+            else oa[u] = fmaf(oa[u], fa, ob[u] * fb);
+          }
           if (pc.whole) {
             __nv_bfloat16* dst = p.out + (((size_t)geom_node0<MODE>(a, pc.b) + qi) * p.Hq + qh) * D + c0;
 #pragma unroll
@@ -1001,14 +1150,30 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
             }
           } else {
             float* dst = p.part_o + (slot * kRowsPerCta + r_local) * D + c0;
+            if constexpr (kWide) {
+              // (whole 32-byte sectors: every piece comes this way)
+              st_global_32(dst, oa);
+              st_global_32(dst + 8, oa + 8);
+            } else {
 #pragma unroll
-            for (int u = 0; u < 4; ++u)
-              *reinterpret_cast<float4*>(dst + 4 * u) = make_float4(oa[4 * u], oa[4 * u + 1], oa[4 * u + 2], oa[4 * u + 3]);
+              for (int u = 0; u < 4; ++u)
+                *reinterpret_cast<float4*>(dst + 4 * u) = make_float4(oa[4 * u], oa[4 * u + 1], oa[4 * u + 2], oa[4 * u + 3]);
+            }
           }
         }
         if (row_ok && !pc.whole && half == 0)
           p.part_lse[slot * kRowsPerCta + r_local] = Ltot > 0.f ? (M + __log2f(Ltot)) * (float)kLn2 : -INFINITY;
         tc_fence_before();
+        if (have_next) {
+          // the other warp of the pair has read O too before either lets the next
+          // piece's first P.V write it
+          mbar_arrive(smem_u32(&bars->pair[quad]));
+          if (!__all_sync(kFull, mbar_wait(smem_u32(&bars->pair[quad]), n_epi & 1, abort))) {
+            ok = false;
+            break;
+          }
+          ++n_epi;
+        }
       }
       pc = pn;
       rc = rn;
@@ -1034,6 +1199,10 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
 // pieces of the shared unit that holds it.
 constexpr int kCombineWarps = kCombineThreads / 32;
 constexpr int kCombChunk = 8;
+// Rows a warp merges, one after another: over a shared prefix every row has
+// pieces to merge, and the schedule's divisions before them are paid per block.
+template <int MODE>
+constexpr int combine_rows = MODE == kModeShared ? 8 : 1;
 
 struct CombParams {
   const float* part_o;
@@ -1104,8 +1273,6 @@ attn_combine_kernel(const CombParams p) {
   const int sb = MODE == kModeShared ? b + 1 : b;  // the schedule's sequence
   const int g = hr / a.RG, rg = hr % a.RG;
   const int G = p.Hq / a.Hkv;
-  const int r = blockIdx.y * kCombineWarps + warp;
-  const int row = rg * kRowsPerCta + r;
   __shared__ long long s_T;
   __shared__ int s_cfirst, s_clast, s_stat[kCombineWarps];
   if (warp == 0) {  // the schedule depends only on prefix_len, not on the attention kernel
@@ -1122,18 +1289,6 @@ attn_combine_kernel(const CombParams p) {
   __syncthreads();
   const long long T = s_T;
   const int c_first = s_cfirst, c_last = s_clast;
-  // kModeShared: the shared unit, CTAs and row that hold this warp's row
-  int us = 0, us_first = 0, us_last = -1, rs = 0;
-  if (MODE == kModeShared) {
-    const int tiles = geom_tiles<MODE>(a, 0);
-    const int at = b * a.n * G + row;
-    us = g * a.RGs + at / kRowsPerCta;
-    rs = at % kRowsPerCta;
-    if (tiles > 0 && row < a.n * G) {
-      us_first = cta_of_tile((long long)us * tiles, T, a.C);
-      us_last = cta_of_tile((long long)us * tiles + tiles - 1, T, a.C);
-    }
-  }
   griddep_wait();
   griddep_launch_dependents();  // the next kernel's prologue may overlap this one
   if (blockIdx.x == 0 && blockIdx.y == 0) {
@@ -1149,20 +1304,34 @@ attn_combine_kernel(const CombParams p) {
     }
   }
   const int valid = min(kRowsPerCta, a.n * G - rg * kRowsPerCta);
-  if ((MODE != kModeShared && c_first == c_last) || r >= valid) return;
-  constexpr int DPL = D / 32;  // output dims per lane
-  float M = -INFINITY, wsum = 0.f;
-  float acc[DPL];
+  if (MODE != kModeShared && c_first == c_last) return;
+  constexpr int kRows = combine_rows<MODE>;  // per warp
+  constexpr int DPL = D / 32;                // output dims per lane
+  for (int q = 0; q < kRows; ++q) {
+    const int r = (blockIdx.y * kRows + q) * kCombineWarps + warp;
+    if (r >= valid) return;
+    const int row = rg * kRowsPerCta + r;
+    float M = -INFINITY, wsum = 0.f;
+    float acc[DPL];
 #pragma unroll
-  for (int t = 0; t < DPL; ++t) acc[t] = 0.f;
-  if (MODE == kModeShared && us_last >= us_first) combine_pieces<D>(p, T, us, us_first, us_last, rs, lane, M, wsum, acc);
-  combine_pieces<D>(p, T, geom_unit<MODE>(a, sb, hr), c_first, c_last, r, lane, M, wsum, acc);
-  const int i = row / G, h = g * G + row % G;
-  __nv_bfloat16* dst = p.out + (((size_t)b * a.n + i) * p.Hq + h) * D + lane * DPL;
-  const float inv = wsum > 0.f ? 1.f / wsum : 0.f;
+    for (int t = 0; t < DPL; ++t) acc[t] = 0.f;
+    if (MODE == kModeShared) {
+      // the shared unit, CTAs and row that hold this row
+      const int tiles = geom_tiles<MODE>(a, 0);
+      const int at = b * a.n * G + row;
+      const int us = g * a.RGs + at / kRowsPerCta;
+      if (tiles > 0)
+        combine_pieces<D>(p, T, us, cta_of_tile((long long)us * tiles, T, a.C),
+                          cta_of_tile((long long)us * tiles + tiles - 1, T, a.C), at % kRowsPerCta, lane, M, wsum, acc);
+    }
+    combine_pieces<D>(p, T, geom_unit<MODE>(a, sb, hr), c_first, c_last, r, lane, M, wsum, acc);
+    const int i = row / G, h = g * G + row % G;
+    __nv_bfloat16* dst = p.out + (((size_t)b * a.n + i) * p.Hq + h) * D + lane * DPL;
+    const float inv = wsum > 0.f ? 1.f / wsum : 0.f;
 #pragma unroll
-  for (int t = 0; t < DPL; t += 2)
-    *reinterpret_cast<__nv_bfloat162*>(dst + t) = __floats2bfloat162_rn(acc[t] * inv, acc[t + 1] * inv);
+    for (int t = 0; t < DPL; t += 2)
+      *reinterpret_cast<__nv_bfloat162*>(dst + t) = __floats2bfloat162_rn(acc[t] * inv, acc[t + 1] * inv);
+  }
 }
 
 // ------------------------------------------------------------------- host
@@ -1279,7 +1448,7 @@ static cudaError_t launch_tc(const AttnCall& k, cudaStream_t s) {
   p.scale_log2 = k.scale * 1.4426950408889634f;
   p.probe_ns = attention_wait_probe_ns();
   p.early = k.early ? 1 : 0;
-  const size_t smem = TcLayout<D>::kSmemBytes;
+  const size_t smem = TcLayout<D, kWideTiles<MODE>>::kSmemBytes;
   cudaError_t e = ensure_smem_limit((const void*)attn_tc_kernel<D, MODE>, smem);
   if (e != cudaSuccess) return e;
 
@@ -1290,7 +1459,7 @@ static cudaError_t launch_tc(const AttnCall& k, cudaStream_t s) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(p.geo.C);
-  cfg.blockDim = dim3(kTcThreads);
+  cfg.blockDim = dim3(kWideTiles<MODE> ? kWideThreads : kTcThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cfg.attrs = attr;
@@ -1307,7 +1476,7 @@ static cudaError_t launch_tc(const AttnCall& k, cudaStream_t s) {
   cp.geo = p.geo;
   cp.Hq = Hq;
   cudaLaunchConfig_t cfg2 = {};
-  cfg2.gridDim = dim3((unsigned)((size_t)B * Hkv * p.geo.RG), kRowsPerCta / kCombineWarps);
+  cfg2.gridDim = dim3((unsigned)((size_t)B * Hkv * p.geo.RG), kRowsPerCta / kCombineWarps / combine_rows<MODE>);
   cfg2.blockDim = dim3(kCombineThreads);
   cfg2.dynamicSmemBytes = 0;
   cfg2.stream = s;
