@@ -964,7 +964,9 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
           ok = false;
           break;
         }
-        if (MODE != kModePlain) {
+        // (wide tiles have no window: all but a range's last tile and the tree's are seen whole by every row)
+        const bool whole_tile = kWide && t < pc.ptiles && piece_key0<MODE>(pc, t) + kBN <= pc.L;
+        if (MODE != kModePlain && !whole_tile) {
           // Values of keys that no row sees (past the prefix, between sinks and
           // window, another sequence's tree) may be anything, NaN included, and
           // 0 x NaN is NaN: this half's such rows of V are zeroed before P says
@@ -1001,34 +1003,36 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
 #pragma unroll
           for (int hh = 0; hh < KW / 32; ++hh) {
             float* xh = x + hh * 32;
-            const int key0 = (tree ? (t - pc.ptiles) * kBN : piece_key0<MODE>(pc, t)) + (kWide ? hh : half) * 32;
-            const int k1 = tree ? a.n : pc.L;
-            // visibility of 32 keys as one bit mask, built the same way on every
-            // tile (so the code stays hot in the instruction cache): keys below
-            // the piece's end, then the ancestor bits (tree keys) or the window's
-            // lower bound (prefix keys)
-            const int lim = k1 - key0;
-            uint32_t vm = low_bits(lim);
-            const uint64_t mw = key0 >= 64 ? rc.mw1 : rc.mw0;
-            const uint32_t tree_bits = (uint32_t)(mw >> (key0 & 63));
-            const int lo_cut = win_lo - key0;  // prefix keys below it are outside the window
-            uint32_t win_bits =
-                (MODE == kModeShared || a.window == 0 || lo_cut <= 0) ? 0xffffffffu : (lo_cut >= 32 ? 0u : ~((1u << lo_cut) - 1u));
-            if (MODE == kModeSinks) win_bits |= low_bits(a.sinks - key0);
-            vm &= tree ? tree_bits : win_bits;
-            if (!row_ok) vm = 0u;
-            if (MODE != kModeShared && tree && a.window > 0) {  // the window on tree keys' positions (rare; warp-uniform)
-              const int grp = key0 >> 5;
-              const int tsel = grp == 0 ? rc.tpos[0] : grp == 1 ? rc.tpos[1] : grp == 2 ? rc.tpos[2] : rc.tpos[3];
+            if (!whole_tile) {
+              const int key0 = (tree ? (t - pc.ptiles) * kBN : piece_key0<MODE>(pc, t)) + (kWide ? hh : half) * 32;
+              const int k1 = tree ? a.n : pc.L;
+              // visibility of 32 keys as one bit mask, built the same way on every
+              // tile (so the code stays hot in the instruction cache): keys below
+              // the piece's end, then the ancestor bits (tree keys) or the window's
+              // lower bound (prefix keys)
+              const int lim = k1 - key0;
+              uint32_t vm = low_bits(lim);
+              const uint64_t mw = key0 >= 64 ? rc.mw1 : rc.mw0;
+              const uint32_t tree_bits = (uint32_t)(mw >> (key0 & 63));
+              const int lo_cut = win_lo - key0;  // prefix keys below it are outside the window
+              uint32_t win_bits =
+                  (MODE == kModeShared || a.window == 0 || lo_cut <= 0) ? 0xffffffffu : (lo_cut >= 32 ? 0u : ~((1u << lo_cut) - 1u));
+              if (MODE == kModeSinks) win_bits |= low_bits(a.sinks - key0);
+              vm &= tree ? tree_bits : win_bits;
+              if (!row_ok) vm = 0u;
+              if (MODE != kModeShared && tree && a.window > 0) {  // the window on tree keys' positions (rare; warp-uniform)
+                const int grp = key0 >> 5;
+                const int tsel = grp == 0 ? rc.tpos[0] : grp == 1 ? rc.tpos[1] : grp == 2 ? rc.tpos[2] : rc.tpos[3];
 #pragma unroll
-              for (int cc = 0; cc < 32; ++cc) {
-                const int kpos = __shfl_sync(kFull, tsel, cc);  // every lane takes part
-                if (kpos < win_lo && !(MODE == kModeSinks && kpos < a.sinks)) vm &= ~(1u << cc);
+                for (int cc = 0; cc < 32; ++cc) {
+                  const int kpos = __shfl_sync(kFull, tsel, cc);  // every lane takes part
+                  if (kpos < win_lo && !(MODE == kModeSinks && kpos < a.sinks)) vm &= ~(1u << cc);
+                }
               }
-            }
-            if (__any_sync(kFull, vm != 0xffffffffu)) {  // most prefix tiles see every key
+              if (__any_sync(kFull, vm != 0xffffffffu)) {  // most prefix tiles see every key
 #pragma unroll
-              for (int cc = 0; cc < 32; ++cc) xh[cc] = ((vm >> cc) & 1u) ? xh[cc] : -INFINITY;
+                for (int cc = 0; cc < 32; ++cc) xh[cc] = ((vm >> cc) & 1u) ? xh[cc] : -INFINITY;
+              }
             }
             float m4[4] = {fmax3(xh[0], xh[1], xh[2]), fmax3(xh[3], xh[4], xh[5]), fmax3(xh[6], xh[7], xh[8]),
                            fmax3(xh[9], xh[10], xh[11])};
@@ -1202,7 +1206,7 @@ constexpr int kCombChunk = 8;
 // Rows a warp merges, one after another: over a shared prefix every row has
 // pieces to merge, and the schedule's divisions before them are paid per block.
 template <int MODE>
-constexpr int combine_rows = MODE == kModeShared ? 8 : 1;
+constexpr int combine_rows = MODE == kModeShared ? 2 : 1;
 
 struct CombParams {
   const float* part_o;
