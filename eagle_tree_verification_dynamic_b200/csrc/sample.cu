@@ -1311,17 +1311,16 @@ accept_sampling_kernel(const T* __restrict__ tgt, const T* __restrict__ dft, con
         draw_kept<T>(tm, sl, s, u, [&](int id, float) { bonus[b] = id; });
         drawn = true;
       } else {
-        double f = 0.0;
-        each<T>(sl, [&](float x, int id) { f += residual(x, id); });
-        F = team_sum(tm, ws, f);
-        if (F > 0.0) {
-          // integer weights of the residual, their sum about 2^60
-          const double scale = 1152921504606846976.0 / F;
-          auto g = [&](float x, int id) { return (u64)(residual(x, id) * scale); };
-          u64 W = 0, unused = 0;
-          each<T>(sl, [&](float x, int id) { W += g(x, id); });
-          tm.sums2(W, unused);
-          select<T>(tm, sl, (u64)(u * (double)W), g, [&](int id, float) { bonus[b] = id; });
+        // integer weights of the residual, of a total F(t) <= 1 as 2^60
+        auto g = [&](float x, int id) { return (u64)(residual(x, id) * 1152921504606846976.0); };
+        u64 mine = 0, W = 0, before;
+        each<T>(sl, [&](float x, int id) { mine += g(x, id); });
+        const auto x = tm.tell<false>(mine, 0);
+        for (int r2 = 0; r2 < tm.size; ++r2) W += x[0][r2];
+        if (W) {
+          const u64 thr = (u64)(u * (double)W);
+          if (owner_of(x[0], tm.size, thr, before) == tm.rank)
+            select_local<T>(sm, sl, thr - before, g, [&](int id, float) { bonus[b] = id; });
           drawn = true;
         }
       }
