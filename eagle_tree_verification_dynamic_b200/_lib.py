@@ -174,6 +174,11 @@ def _stream(device) -> ctypes.c_void_p:
     return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
 
 
+def _on(device):
+    """The device a call launches on, made current (the C call launches on the current one)."""
+    return torch.cuda.device(device)
+
+
 def _dtype_code(t: torch.Tensor) -> int:
     if t.dtype == torch.float32:
         return F32
@@ -338,10 +343,11 @@ def tree_attention_into(q, k_cache, v_cache, prefix_len, k_tree, v_tree, mask, p
                         window: int = 0, scale: float = 0.0, sinks: int = 0):
     B, n, Hq, D = q.shape
     Hkv, Lmax = k_cache.shape[1], k_cache.shape[2]
-    _check(lib().eagle_tree_attention_with_sinks(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(prefix_len), Lmax,
-                                                 _ptr(k_tree), _ptr(v_tree), _ptr(mask), _ptr(pos), B, n, Hq, Hkv, D,
-                                                 window, sinks, scale, _ptr(out), _ptr(ws), ws.numel(),
-                                                 _stream(q.device)), "eagle_tree_attention")
+    with _on(q.device):
+        _check(lib().eagle_tree_attention_with_sinks(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(prefix_len), Lmax,
+                                                     _ptr(k_tree), _ptr(v_tree), _ptr(mask), _ptr(pos), B, n, Hq, Hkv, D,
+                                                     window, sinks, scale, _ptr(out), _ptr(ws), ws.numel(),
+                                                     _stream(q.device)), "eagle_tree_attention")
 
 
 def tree_attention(q, k_cache, v_cache, prefix_len, k_tree, v_tree, mask, pos=None, window: int = 0,
@@ -383,10 +389,11 @@ def tree_attention_paged_into(q, k_pages, v_pages, block_table, prefix_len, k_tr
     """k_pages / v_pages [num_pages][Hkv][page_size][D] bf16, block_table [B][pages_per_seq] int32."""
     B, n, Hq, D = q.shape
     num_pages, Hkv, ps = k_pages.shape[0], k_pages.shape[1], k_pages.shape[2]
-    _check(lib().eagle_tree_attention_paged_with_sinks(
-        _ptr(q), _ptr(k_pages), _ptr(v_pages), num_pages, ps, _ptr(block_table), block_table.shape[1],
-        _ptr(prefix_len), _ptr(k_tree), _ptr(v_tree), _ptr(mask), _ptr(pos), B, n, Hq, Hkv, D, window, sinks, scale,
-        _ptr(out), _ptr(ws), ws.numel(), _stream(q.device)), "eagle_tree_attention_paged")
+    with _on(q.device):
+        _check(lib().eagle_tree_attention_paged_with_sinks(
+            _ptr(q), _ptr(k_pages), _ptr(v_pages), num_pages, ps, _ptr(block_table), block_table.shape[1],
+            _ptr(prefix_len), _ptr(k_tree), _ptr(v_tree), _ptr(mask), _ptr(pos), B, n, Hq, Hkv, D, window, sinks, scale,
+            _ptr(out), _ptr(ws), ws.numel(), _stream(q.device)), "eagle_tree_attention_paged")
 
 
 def tree_attention_paged(q, k_pages, v_pages, block_table, prefix_len, k_tree, v_tree, mask, pos=None,
@@ -415,10 +422,11 @@ def tree_attention_shared_into(q, k_shared, v_shared, shared_len, k_cache, v_cac
                                out, ws, scale: float = 0.0):
     B, n, Hq, D = q.shape
     Hkv, Lmax = k_cache.shape[1], k_cache.shape[2]
-    _check(lib().eagle_tree_attention_shared(
-        _ptr(q), _ptr(k_shared), _ptr(v_shared), k_shared.shape[1], _ptr(shared_len), _ptr(k_cache), _ptr(v_cache),
-        _ptr(prefix_len), Lmax, _ptr(k_tree), _ptr(v_tree), _ptr(mask), B, n, Hq, Hkv, D, scale, _ptr(out), _ptr(ws),
-        ws.numel(), _stream(q.device)), "eagle_tree_attention_shared")
+    with _on(q.device):
+        _check(lib().eagle_tree_attention_shared(
+            _ptr(q), _ptr(k_shared), _ptr(v_shared), k_shared.shape[1], _ptr(shared_len), _ptr(k_cache), _ptr(v_cache),
+            _ptr(prefix_len), Lmax, _ptr(k_tree), _ptr(v_tree), _ptr(mask), B, n, Hq, Hkv, D, scale, _ptr(out), _ptr(ws),
+            ws.numel(), _stream(q.device)), "eagle_tree_attention_shared")
 
 
 def tree_attention_shared(q, k_shared, v_shared, shared_len, k_cache, v_cache, prefix_len, k_tree, v_tree, mask,
@@ -449,11 +457,12 @@ def tree_attention_shared_paged_into(q, k_pages, v_pages, shared_table, shared_l
     """shared_table [shared_pages] int32: the pages of the keys that every sequence begins with."""
     B, n, Hq, D = q.shape
     num_pages, Hkv, ps = k_pages.shape[0], k_pages.shape[1], k_pages.shape[2]
-    _check(lib().eagle_tree_attention_shared_paged(
-        _ptr(q), _ptr(k_pages), _ptr(v_pages), num_pages, ps, _ptr(shared_table), shared_table.shape[0],
-        _ptr(shared_len), _ptr(block_table), block_table.shape[1], _ptr(prefix_len), _ptr(k_tree), _ptr(v_tree),
-        _ptr(mask), B, n, Hq, Hkv, D, scale, _ptr(out), _ptr(ws), ws.numel(), _stream(q.device)),
-        "eagle_tree_attention_shared_paged")
+    with _on(q.device):
+        _check(lib().eagle_tree_attention_shared_paged(
+            _ptr(q), _ptr(k_pages), _ptr(v_pages), num_pages, ps, _ptr(shared_table), shared_table.shape[0],
+            _ptr(shared_len), _ptr(block_table), block_table.shape[1], _ptr(prefix_len), _ptr(k_tree), _ptr(v_tree),
+            _ptr(mask), B, n, Hq, Hkv, D, scale, _ptr(out), _ptr(ws), ws.numel(), _stream(q.device)),
+            "eagle_tree_attention_shared_paged")
 
 
 def tree_attention_shared_paged(q, k_pages, v_pages, shared_table, shared_len, block_table, prefix_len, k_tree, v_tree,
@@ -537,8 +546,9 @@ def sample_into(logits, uniforms, sampling: Optional[Sampling], tokens, logprob=
     """eagle_sample into preallocated tokens [rows] int32 and logprob [rows] f32 (or None)."""
     rows, V = logits.shape
     st = None if sampling is None else ctypes.byref(sampling.struct())
-    _check(lib().eagle_sample(_ptr(logits), _dtype_code(logits), rows, V, logits.stride(0) if rows > 1 else V, st,
-                              _ptr(uniforms), _ptr(tokens), _ptr(logprob), _stream(logits.device)), "eagle_sample")
+    with _on(logits.device):
+        _check(lib().eagle_sample(_ptr(logits), _dtype_code(logits), rows, V, logits.stride(0) if rows > 1 else V, st,
+                                  _ptr(uniforms), _ptr(tokens), _ptr(logprob), _stream(logits.device)), "eagle_sample")
 
 
 def sample(logits: torch.Tensor, uniforms: torch.Tensor, sampling: Optional[Sampling] = None):
@@ -568,11 +578,12 @@ def accept_into(target_logits, tokens, parents, draft_row, depth, uniforms, draf
     ddt = _dtype_code(draft_logits) if draft_logits is not None else 0
     rule = SAMPLE_WITHOUT_REPLACEMENT if without_replacement else SAMPLE_WITH_REPLACEMENT
     if sampling is not None:
-        _check(lib().eagle_accept_with_sampling(
-            _ptr(target_logits), _dtype_code(target_logits), _ptr(draft_logits), ddt, _ptr(draft_lse), R, _ptr(tokens),
-            _ptr(parents), _ptr(draft_row), _ptr(uniforms), rule, ctypes.byref(sampling.struct()), B, n, V, depth,
-            _ptr(accepted_len), _ptr(path), _ptr(bonus), _ptr(ws), ws.numel(), _stream(target_logits.device)),
-            "eagle_accept_with_sampling")
+        with _on(target_logits.device):
+            _check(lib().eagle_accept_with_sampling(
+                _ptr(target_logits), _dtype_code(target_logits), _ptr(draft_logits), ddt, _ptr(draft_lse), R,
+                _ptr(tokens), _ptr(parents), _ptr(draft_row), _ptr(uniforms), rule, ctypes.byref(sampling.struct()), B,
+                n, V, depth, _ptr(accepted_len), _ptr(path), _ptr(bonus), _ptr(ws), ws.numel(),
+                _stream(target_logits.device)), "eagle_accept_with_sampling")
         return
     _check(lib().eagle_accept_with_rule(_ptr(target_logits), _dtype_code(target_logits), _ptr(draft_logits), ddt,
                                         _ptr(draft_lse), R, _ptr(tokens), _ptr(parents), _ptr(draft_row),

@@ -61,7 +61,7 @@ constexpr int kCombineThreads = 128;
 // WIDE: how the two softmax warps of a lane quarter share the tiles.  Narrow: each
 // tile's keys in halves (32 per thread), three S buffers; the shortest way from
 // a tile to its product, for CTAs with a handful of tiles.  Wide: whole tiles in
-// turn (64 keys per thread), four S buffers, O_A over a piece's even tiles and
+// turn (64 keys per thread), four S buffers, O_A over the CTA's even tiles and
 // O_B over its odd ones: the waits, the TMEM round trips and the reductions of a
 // tile come once per 64 keys and overlap the other warps' tile, for CTAs that
 // stream many tiles.
@@ -96,6 +96,7 @@ struct TcLayout {
   static_assert(kSmemBytes <= kSmemOptIn, "shared memory");
   static_assert(kXchOff + 2 * 128 * 8 <= kHdrBytes, "header");
   static_assert(kColOB + D <= kTmemCols, "TMEM");
+  static_assert(!WIDE || kSBufs % 2 == 0, "a buffer always the same warps'");
 };
 
 struct TcBars {
@@ -565,7 +566,7 @@ __device__ __forceinline__ void mma_outputs(const AttnGeom& a, TcBars* bars, uin
     tc_fence_after();
     const uint64_t db = v_desc + (uint64_t)(st * (Lay::kStageBytes >> 4));
     const uint32_t t_p = tmem + Lay::kColS + (uint32_t)((j % NB) * kBN);
-    const uint32_t t_o = tmem + ((tix & 1) ? Lay::kColOB : Lay::kColOA);
+    const uint32_t t_o = tmem + ((j & 1) ? Lay::kColOB : Lay::kColOA);
     const uint32_t more = tix >= 2 ? 1u : 0u;  // an accumulator starts at the piece's first even, first odd tile
     if (elect_one()) {
 #pragma unroll
@@ -957,7 +958,11 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
       const int win_lo = rc.qpos - a.window + 1;
       float m_used = -INFINITY, l = 0.f;  // reference max (scaled, log2) and row sum of this half
       for (int t = pc.tb; t < pc.te; ++t, ++jg) {
-        if (kWide && ((t - pc.tb) & 1) != half) continue;  // the other four warps' tile
+        // Wide: even tiles of the CTA are the first four warps', odd ones the
+        // others'.  (With an even number of S buffers a buffer is always the same
+        // warps', which so wait for each phase of its barrier in turn: a parity
+        // wait that skips a phase would pass too early.)
+        if (kWide && (jg & 1) != half) continue;
         const int sbuf = jg % NB;
         if (!__all_sync(kFull, mbar_wait(smem_u32(&bars->s_full[sbuf]), (uint32_t)(jg / NB) & 1u, abort, 2000000000ull,
                                          kSoftmaxSleepNs))) {
@@ -1106,6 +1111,13 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
       // writes its half of the output columns from both accumulators.
       if (warp_live) {
         const int jl = jg - 1;
+        // (wide, the last tile not these warps': S of it first, which was issued
+        // once PV(jl - NB) was done, so that the wait below is for this phase)
+        if (kWide && (jl & 1) != half &&
+            !__all_sync(kFull, mbar_wait(smem_u32(&bars->s_full[jl % NB]), (uint32_t)(jl / NB) & 1u, abort))) {
+          ok = false;
+          break;
+        }
         if (!__all_sync(kFull, mbar_wait(smem_u32(&bars->pv_done[jl % NB]), (uint32_t)(jl / NB) & 1u, abort))) {
           ok = false;
           break;
@@ -1136,8 +1148,8 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
           if (!row_ok) continue;
 #pragma unroll
           for (int u = 0; u < 16; ++u) {
-            // (wide: a piece of one tile never wrote O_B)
-            if (kWide) oa[u] = fmaf(oa[u], fa, fb > 0.f ? ob[u] * fb : 0.f);
+            // (wide: a piece of one tile wrote only one of them)
+            if (kWide) oa[u] = (fa > 0.f ? oa[u] * fa : 0.f) + (fb > 0.f ? ob[u] * fb : 0.f);
             else oa[u] = fmaf(oa[u], fa, ob[u] * fb);
           }
           if (pc.whole) {

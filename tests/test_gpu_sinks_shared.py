@@ -205,3 +205,61 @@ def test_on_another_stream_and_replayed_from_graphs():
     assert torch.isfinite(o1).all()       # 5: the sinks alone (30 also sees keys that hide() made NaN)
     et.check_attention_status(ws1)
     et.check_attention_status(ws2)
+
+
+def test_a_wait_that_gives_up_is_reported_and_the_next_call_is_right():
+    """The wide kernel's roles end when a bounded wait runs out (status 1); nothing stays behind."""
+    c = Case(12, 3, 20, 8, 2, 128, [200, 40, 260], Ls=300)
+    args = (c.q, c.ks, c.vs, c.slen, c.kc, c.vc, c.plen, c.kt, c.vt, c.mask)
+    try:
+        et.attention_wait_probe(1_000_000)
+        with pytest.raises(et.EagleError, match="status 1"):
+            et.tree_attention_shared(*args)
+    finally:
+        et.attention_wait_probe(0)
+    c.check(et.tree_attention_shared(*args))
+
+
+def test_shared_paged_without_shared_pages():
+    c = Case(13, 3, 20, 8, 2, 64, [200, 40, 260], Ls=0)
+    state = c.rng.bit_generator.state
+    kp, table = paged(c.kc, c.lens, 32, c.rng)
+    c.rng.bit_generator.state = state
+    vp, _ = paged(c.vc, c.lens, 32, c.rng)
+    none = torch.empty(0, dtype=torch.int32, device="cuda")
+    c.check(et.tree_attention_shared_paged(c.q, kp, vp, none, c.slen, table, c.plen, c.kt, c.vt, c.mask))
+
+
+def test_shared_length_is_clamped_and_read_at_the_call():
+    c = Case(14, 2, 12, 4, 2, 128, [70, 9], Ls=150)
+    args = (c.q, c.ks, c.vs, c.slen, c.kc, c.vc, c.plen, c.kt, c.vt, c.mask)
+    want = et.tree_attention_shared(*args)
+    c.slen.fill_(10_000)                  # past the buffer: all of it
+    assert torch.equal(et.tree_attention_shared(*args), want)
+    c.slen.fill_(-5)                      # none of it
+    c.Ls = 0
+    c.check(et.tree_attention_shared(*args))
+
+
+@pytest.mark.parametrize("B,n,Hq,Hkv,D,Ls,top", [(150, 7, 6, 2, 64, 200, 90), (150, 7, 6, 2, 64, 0, 1),
+                                                  (90, 3, 8, 4, 128, 70, 140), (200, 1, 4, 4, 128, 500, 60),
+                                                  (33, 70, 4, 1, 64, 129, 300)])
+def test_many_sequences_and_pieces(B, n, Hq, Hkv, D, Ls, top):
+    """More units than CTAs, pieces of one tile after another, rows of one unit in two shared units."""
+    lens = np.random.default_rng(3).integers(0, top, B)
+    c = Case(15, B, n, Hq, Hkv, D, lens, Lmax=top, Ls=Ls)
+    for _ in range(3):
+        c.check(et.tree_attention_shared(c.q, c.ks, c.vs, c.slen, c.kc, c.vc, c.plen, c.kt, c.vt, c.mask))
+
+
+def test_attention_refusals():
+    c = Case(16, 2, 6, 4, 2, 64, [20, 9], Ls=30)
+    good = [c.q, c.ks, c.vs, c.slen, c.kc, c.vc, c.plen, c.kt, c.vt, c.mask]
+    for i, bad in ((0, c.q.float()), (0, c.q[0]), (1, c.ks[:1]), (2, c.vs[:, :5]), (3, c.slen.long()), (4, c.kc[:1]),
+                   (5, c.vc[:, :, :, :32]), (6, c.plen[:1]), (7, c.kt[:, :3]), (8, c.vt.cpu()), (9, c.mask[:, :3])):
+        args = list(good)
+        args[i] = bad
+        with pytest.raises(et.EagleError):
+            et.tree_attention_shared(*args)
+    with pytest.raises(et.EagleError):
+        et.tree_attention(c.q, c.kc, c.vc, c.plen, c.kt, c.vt, c.mask, c.pos, window=8, sinks=-1)
