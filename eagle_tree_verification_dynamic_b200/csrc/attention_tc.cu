@@ -19,8 +19,8 @@
 //   warp 0      producer: Q of each unit (TMA box, or a gather when G does not
 //               divide 128) into one of two Q buffers; K and V tiles into a
 //               ring of stages (128-byte swizzle, no multicast); TMEM owner
-//   warp 1      one thread issues tcgen05.mma: S = Q K^T into one of two TMEM
-//               S buffers, at most one tile ahead of PV; O += P V into TMEM,
+//   warp 1      one thread issues tcgen05.mma: S = Q K^T into one of three TMEM
+//               S buffers, at most two tiles ahead of PV; O += P V into TMEM,
 //               each tile's keys 0..31 into O_A and keys 32..63 into O_B
 //   warps 2-9   softmax, two warps per TMEM lane quarter: thread r owns query
 //               row r, one warp the first 32 keys of every tile (and O_A), the
@@ -28,9 +28,12 @@
 //               window / tree bitmask, keeps its own running reference max
 //               (re-based only when it grows by > 8 in log2 units, then its O
 //               and row sum are rescaled in TMEM) and writes P = 2^(x - m) as
-//               bf16 into one of two swizzled P buffers.  At the end of a
-//               unit's piece the pair exchanges (max, sum) through shared
-//               memory, merges O_A and O_B, and writes the output or partial
+//               bf16 over the S it has read.  At the end of a unit's piece the
+//               pair exchanges (max, sum) through shared memory, merges O_A and
+//               O_B, and writes the output or partial
+// Over a shared prefix (wide tiles, 352 threads) the softmax warps of a quarter
+// take whole tiles in turn, O_A over the CTA's even tiles and O_B over its odd
+// ones, and warp 10 issues the O products while warp 1 issues the S ones.
 //
 // Every mbarrier wait is bounded (about 2 s of wall time); a timeout sets an
 // abort flag that ends all roles, records a per-CTA status word and still
@@ -475,9 +478,11 @@ __device__ __forceinline__ uint32_t low_bits(int count) {
   return count >= 32 ? 0xffffffffu : (count > 0 ? (1u << count) - 1u : 0u);
 }
 
-// A batch over a shared prefix is bound by arithmetic, with about a hundred tiles
-// and more a CTA: wide (32 sequences over 4096 shared keys 205 -> @@ us, 16 over
-// 32763, 80-node trees, 1740 -> @@ us).
+// A batch over a shared prefix is bound by the chain S, softmax, P, O of its tiles,
+// a hundred and more a CTA: wide (32 sequences over 4096 shared keys 291 -> 215 us,
+// 16 over 32763 with 80-node trees 1740 -> 1250 us).  With sinks and a window a CTA
+// has few tiles, narrow: 24.5 us either way at one sequence (window 2048),
+// 87 us against 93 wide at 32 sequences.
 template <int MODE>
 constexpr bool kWideTiles = MODE == kModeShared;
 
@@ -1216,7 +1221,9 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
 constexpr int kCombineWarps = kCombineThreads / 32;
 constexpr int kCombChunk = 8;
 // Rows a warp merges, one after another: over a shared prefix every row has
-// pieces to merge, and the schedule's divisions before them are paid per block.
+// pieces to merge, and the schedule's divisions before them are paid per block
+// (1, 2, 4, 8 rows a warp: 54, 50, 52, 66 us at 4 sequences, 224, 214, 212, 216
+// at 32).
 template <int MODE>
 constexpr int combine_rows = MODE == kModeShared ? 2 : 1;
 

@@ -348,7 +348,8 @@ EAGLE_API eagle_status eagle_accept(const void* target_logits, int target_dtype,
 /* -------------------------------------------- sampling under parameters
  * What a request asks of its samples.  DEVICE arrays, one entry per row (for
  * the walk: per sequence); a NULL array leaves that parameter off for all.
- *   temperature  T > 0 (NULL: 1); T <= 0 or NaN: greedy, the argmax alone
+ *   temperature  T > 0 (NULL: 1; below 2^-100 as 2^-100); T <= 0 or NaN: greedy,
+ *                the argmax alone
  *   top_k        the k likeliest tokens (ties to the lower id); <= 0 or >= V: off
  *   top_p        of those, the fewest likeliest ones whose probability among
  *                them sums to at least top_p (always one); >= 1 or NaN: off

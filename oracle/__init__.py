@@ -25,6 +25,8 @@ Everything is plain numpy in fp64, written step by step from the pages:
                 resampling (EAGLE-2 "Well-Calibrated Draft Model" formula;
                 aivaro.ru EAGLE-3 answer, section 4 steps 3-4; EAGLE-4
                 write-up, same section as the mask).
+* ``sampling``  sampling under temperature, top-k, top-p and min-p: a token per
+                row, and the acceptance walk with the target so filtered.
 * ``paged``     the prefix cache as pages of a shared pool named by a block
                 table: gather, and compaction into pages.
 * ``sizing``    cost-aware tree sizing: a measured latency table, each

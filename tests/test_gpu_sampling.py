@@ -143,6 +143,28 @@ def test_parameters_that_are_no_numbers():
     assert (big > 400).all()                                             # read as the largest u below 1
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_temperatures_near_the_smallest_float(dtype):
+    """Acts as greedy where logits differ, and below 2^-100 as 2^-100: equal weights for logits 1e-37 apart (a ratio of
+    1 - 1.3e-7, so that a draw in the middle of a token's share is that token's: 500 times 1.3e-7 of a share off)."""
+    V = 1000
+    rng = np.random.default_rng(5)
+    x = torch.tensor(rng.standard_normal((4, V))).to(DT[dtype]).cuda()
+    T = np.array([1.4e-45, 1e-38, 1e-30, 1e-20], dtype=np.float32)
+    tok, lp = et.sample(x, f32([0.1, 0.9, 0.5, 0.0]), sampling_of(T))
+    top = x.double().cpu().numpy()
+    for r in range(4):
+        ids = np.flatnonzero(top[r] == top[r].max())
+        assert tok[r].item() == ids[int([0.1, 0.9, 0.5, 0.0][r] * len(ids))]
+        assert abs(lp[r].item() + math.log(len(ids))) < 1e-6
+    y = torch.zeros(3, V, dtype=DT[dtype]).cuda()
+    y[:, ::2] = -1e-37
+    want = [0, 501, 999]
+    tok, lp = et.sample(y, f32([(i + 0.5) / V for i in want]), sampling_of([1.4e-45] * 3))
+    assert tok.tolist() == want
+    assert (lp.double().cpu() + math.log(V)).abs().max().item() < 2e-6
+
+
 def test_the_draws_follow_the_distribution():
     """Every u of a fine grid: the tokens' shares are the kept probabilities (each within the grid's two ends)."""
     rng = np.random.default_rng(8)
