@@ -1252,12 +1252,15 @@ __device__ __forceinline__ void combine_pieces(const CombParams& p, long long T,
     float v[kCombChunk][DPL];
 #pragma unroll
     for (int j = 0; j < kCombChunk; ++j) {
-      // a CTA with an empty range wrote no partial: read the first piece's
-      // (always written, finite) and give it weight 0
+      // (a CTA with an empty range wrote no partial)
       const int s = s0 + j;
       const bool live = s < nseg && (all_live || cta_nonempty(c_first + s, T, C));
-      const size_t sl = live ? slot0 + s : slot0;
-      ls[j] = live ? __ldcg(p.part_lse + sl * kRowsPerCta + r) : -INFINITY;
+      ls[j] = -INFINITY;
+#pragma unroll
+      for (int t = 0; t < DPL; ++t) v[j][t] = 0.f;
+      if (!live) continue;
+      const size_t sl = slot0 + s;
+      ls[j] = __ldcg(p.part_lse + sl * kRowsPerCta + r);
       const float* src = p.part_o + (sl * kRowsPerCta + r) * D + lane * DPL;
       if constexpr (DPL == 4) {
         const float4 f = __ldcg(reinterpret_cast<const float4*>(src));
