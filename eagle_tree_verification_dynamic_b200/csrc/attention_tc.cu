@@ -1213,19 +1213,20 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
 //   out = sum_s e^{lse_s - M} O_s / sum_s e^{lse_s - M}
 // One warp per query row (blockIdx.x = unit, blockIdx.y = group of 4 rows);
 // each lane loads its D/32 dims of every piece's partial in one round of
-// independent L2 reads, up to kCombChunk pieces at a time, merged online.
+// independent L2 reads, up to eight pieces at a time, merged online (the modes with
+// sinks or a shared prefix: two rows, four pieces of each).
 // A unit finished inside one CTA is skipped.  Block (0, 0) also folds the
 // per-CTA status words into the workspace header.  In kModeShared the units
 // are the sequences' own, every one left partials, and a row also takes the
 // pieces of the shared unit that holds it.
 constexpr int kCombineWarps = kCombineThreads / 32;
-constexpr int kCombChunk = 8;
 // Rows a warp merges, one after another: over a shared prefix every row has
 // pieces to merge, and the schedule's divisions before them are paid per block
-// (1, 2, 4, 8 rows a warp: 54, 50, 52, 66 us at 4 sequences, 224, 214, 212, 216
-// at 32).
+// (2, 4, 8 rows a warp, two at a time: 48, 46, 52 us at 4 sequences, 198, 194,
+// 192 at 32).  With sinks only cut units do: one row, for latency (1, 2, 4: 30.7,
+// 31.7, 34 us at one long sequence; 87, 87, 83 at 32).
 template <int MODE>
-constexpr int combine_rows = MODE == kModeShared ? 2 : 1;
+constexpr int combine_rows = MODE == kModeShared ? 4 : 1;
 
 struct CombParams {
   const float* part_o;
@@ -1237,55 +1238,78 @@ struct CombParams {
   int Hq;
 };
 
-// The pieces c_first..c_last of one unit (its slots start at c_first + unit),
-// row r of its 128, folded into the running (M, wsum, acc).
-template <int D>
-__device__ __forceinline__ void combine_pieces(const CombParams& p, long long T, int unit, int c_first, int c_last, int r,
-                                               int lane, float& M, float& wsum, float (&acc)[D / 32]) {
+// Where a row's partials are: its pieces in CTAs c_shared.. (n_shared of them, of
+// row r_shared of a shared unit), then those of its own unit in CTAs c_own.., row
+// r_own, `count` in all.  A unit's slots start at its first CTA + its number.
+struct RowPieces {
+  int n_shared, count, c_shared, c_own, r_shared, r_own;
+  size_t slot_shared, slot_own;
+};
+
+// Merge ROWS rows' pieces, up to CHUNK of each per round of loads.
+template <int D, int ROWS, int CHUNK>
+__device__ __forceinline__ void combine_pieces(const CombParams& p, long long T, const RowPieces (&w)[ROWS], int lane,
+                                               float (&wsum)[ROWS], float (&acc)[ROWS][D / 32]) {
   constexpr int DPL = D / 32;  // output dims per lane
   const int C = p.geo.C;
   const bool all_live = T >= C;  // with at least one tile per CTA no range is empty
-  const int nseg = c_last - c_first + 1;
-  const size_t slot0 = (size_t)c_first + unit;
-  for (int s0 = 0; s0 < nseg; s0 += kCombChunk) {
-    float ls[kCombChunk];
-    float v[kCombChunk][DPL];
+  float M[ROWS];
+  int most = 0;
 #pragma unroll
-    for (int j = 0; j < kCombChunk; ++j) {
-      // (a CTA with an empty range wrote no partial)
-      const int s = s0 + j;
-      const bool live = s < nseg && (all_live || cta_nonempty(c_first + s, T, C));
-      ls[j] = -INFINITY;
+  for (int q = 0; q < ROWS; ++q) {
+    M[q] = -INFINITY;
+    wsum[q] = 0.f;
 #pragma unroll
-      for (int t = 0; t < DPL; ++t) v[j][t] = 0.f;
-      if (!live) continue;
-      const size_t sl = slot0 + s;
-      ls[j] = __ldcg(p.part_lse + sl * kRowsPerCta + r);
-      const float* src = p.part_o + (sl * kRowsPerCta + r) * D + lane * DPL;
-      if constexpr (DPL == 4) {
-        const float4 f = __ldcg(reinterpret_cast<const float4*>(src));
-        v[j][0] = f.x; v[j][1] = f.y; v[j][2] = f.z; v[j][3] = f.w;
-      } else {
-        const float2 f = __ldcg(reinterpret_cast<const float2*>(src));
-        v[j][0] = f.x; v[j][1] = f.y;
+    for (int t = 0; t < DPL; ++t) acc[q][t] = 0.f;
+    most = max(most, w[q].count);
+  }
+  for (int s0 = 0; s0 < most; s0 += CHUNK) {
+    float ls[ROWS][CHUNK];
+    float v[ROWS][CHUNK][DPL];
+#pragma unroll
+    for (int q = 0; q < ROWS; ++q) {
+#pragma unroll
+      for (int j = 0; j < CHUNK; ++j) {
+        const int s = s0 + j;
+        const bool sh = s < w[q].n_shared;
+        const int at = sh ? s : s - w[q].n_shared;
+        // (a CTA with an empty range wrote no partial)
+        const bool live = s < w[q].count && (all_live || cta_nonempty((sh ? w[q].c_shared : w[q].c_own) + at, T, C));
+        ls[q][j] = -INFINITY;
+#pragma unroll
+        for (int t = 0; t < DPL; ++t) v[q][j][t] = 0.f;
+        if (!live) continue;
+        const size_t sl = ((sh ? w[q].slot_shared : w[q].slot_own) + at) * kRowsPerCta + (sh ? w[q].r_shared : w[q].r_own);
+        ls[q][j] = __ldcg(p.part_lse + sl);
+        const float* src = p.part_o + sl * D + lane * DPL;
+        if constexpr (DPL == 4) {
+          const float4 f = __ldcg(reinterpret_cast<const float4*>(src));
+          v[q][j][0] = f.x; v[q][j][1] = f.y; v[q][j][2] = f.z; v[q][j][3] = f.w;
+        } else {
+          const float2 f = __ldcg(reinterpret_cast<const float2*>(src));
+          v[q][j][0] = f.x; v[q][j][1] = f.y;
+        }
       }
     }
-    float mc = M;
 #pragma unroll
-    for (int j = 0; j < kCombChunk; ++j) mc = fmaxf(mc, ls[j]);
-    if (mc == -INFINITY) continue;
-    const float f = M > -INFINITY ? __expf(M - mc) : 0.f;
-    wsum *= f;
+    for (int q = 0; q < ROWS; ++q) {
+      float mc = M[q];
 #pragma unroll
-    for (int t = 0; t < DPL; ++t) acc[t] *= f;
+      for (int j = 0; j < CHUNK; ++j) mc = fmaxf(mc, ls[q][j]);
+      if (mc == -INFINITY) continue;
+      const float f = M[q] > -INFINITY ? __expf(M[q] - mc) : 0.f;
+      wsum[q] *= f;
 #pragma unroll
-    for (int j = 0; j < kCombChunk; ++j) {
-      const float w = ls[j] > -INFINITY ? __expf(ls[j] - mc) : 0.f;
-      wsum += w;
+      for (int t = 0; t < DPL; ++t) acc[q][t] *= f;
 #pragma unroll
-      for (int t = 0; t < DPL; ++t) acc[t] = fmaf(w, v[j][t], acc[t]);
+      for (int j = 0; j < CHUNK; ++j) {
+        const float e = ls[q][j] > -INFINITY ? __expf(ls[q][j] - mc) : 0.f;
+        wsum[q] += e;
+#pragma unroll
+        for (int t = 0; t < DPL; ++t) acc[q][t] = fmaf(e, v[q][j][t], acc[q][t]);
+      }
+      M[q] = mc;
     }
-    M = mc;
   }
 }
 
@@ -1299,17 +1323,41 @@ attn_combine_kernel(const CombParams p) {
   const int sb = MODE == kModeShared ? b + 1 : b;  // the schedule's sequence
   const int g = hr / a.RG, rg = hr % a.RG;
   const int G = p.Hq / a.Hkv;
+  const int row0 = rg * kRowsPerCta, valid = min(kRowsPerCta, a.n * G - row0);
+  constexpr int kRows = combine_rows<MODE>;        // per warp,
+  constexpr int kAtOnce = MODE == kModeShared ? 2 : 1;  // as many at a time,
+  constexpr int kChunk = MODE == kModePlain ? 8 : 4;   // so many pieces of each
+  constexpr int kBlockRows = kRows * kCombineWarps;
+  static_assert(kBlockRows <= 32 && kRows % kAtOnce == 0, "a lane per row of the block");
   __shared__ long long s_T;
   __shared__ int s_cfirst, s_clast, s_stat[kCombineWarps];
+  __shared__ int3 s_shared[kBlockRows];  // kModeShared: each row's shared unit, its first and its last CTA
   if (warp == 0) {  // the schedule depends only on prefix_len, not on the attention kernel
-    const long long T = geom_prefix<MODE>(a, geom_seqs<MODE>(a), lane);
-    const long long cum = geom_prefix<MODE>(a, sb, lane);
-    const int tiles = geom_tiles<MODE>(a, sb);
-    if (lane == 0) {  // (64-bit divisions: done before the wait, while the attention runs)
+    const int nb = geom_seqs<MODE>(a);
+    long long T = 0, cum = 0;
+    for (int s = lane; s < nb; s += 32) {
+      const long long v = (long long)(a.Hkv * geom_rg<MODE>(a, s)) * geom_tiles<MODE>(a, s);
+      T += v;
+      if (s < sb) cum += v;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      T += __shfl_xor_sync(kFull, T, o);
+      cum += __shfl_xor_sync(kFull, cum, o);
+    }
+    if (lane == 0) {  // (divisions: done before the wait, while the attention runs)
+      const int tiles = geom_tiles<MODE>(a, sb);
       const long long start = cum + (long long)hr * tiles;
       s_T = T;
       s_cfirst = cta_of_tile(start, T, a.C);
       s_clast = cta_of_tile(start + tiles - 1, T, a.C);
+    }
+    if (MODE == kModeShared && lane < kBlockRows) {
+      const int tiles = geom_tiles<MODE>(a, 0);
+      const int us = g * a.RGs + (b * a.n * G + row0 + (int)blockIdx.y * kBlockRows + lane) / kRowsPerCta;
+      s_shared[lane] = tiles > 0 ? make_int3(us, cta_of_tile((long long)us * tiles, T, a.C),
+                                             cta_of_tile((long long)us * tiles + tiles - 1, T, a.C))
+                                 : make_int3(us, 0, -1);
     }
   }
   __syncthreads();
@@ -1329,34 +1377,43 @@ attn_combine_kernel(const CombParams p) {
       *p.status = st;
     }
   }
-  const int valid = min(kRowsPerCta, a.n * G - rg * kRowsPerCta);
   if (MODE != kModeShared && c_first == c_last) return;
-  constexpr int kRows = combine_rows<MODE>;  // per warp
-  constexpr int DPL = D / 32;                // output dims per lane
-  for (int q = 0; q < kRows; ++q) {
-    const int r = (blockIdx.y * kRows + q) * kCombineWarps + warp;
-    if (r >= valid) return;
-    const int row = rg * kRowsPerCta + r;
-    float M = -INFINITY, wsum = 0.f;
-    float acc[DPL];
+  constexpr int DPL = D / 32;  // output dims per lane
+  for (int q0 = 0; q0 < kRows; q0 += kAtOnce) {
+    const int first = (blockIdx.y * kRows + q0) * kCombineWarps + warp;  // rows first, first + kCombineWarps, ...
+    if (first >= valid) return;
+    RowPieces w[kAtOnce];
+    float wsum[kAtOnce], acc[kAtOnce][DPL];
 #pragma unroll
-    for (int t = 0; t < DPL; ++t) acc[t] = 0.f;
-    if (MODE == kModeShared) {
-      // the shared unit, CTAs and row that hold this row
-      const int tiles = geom_tiles<MODE>(a, 0);
-      const int at = b * a.n * G + row;
-      const int us = g * a.RGs + at / kRowsPerCta;
-      if (tiles > 0)
-        combine_pieces<D>(p, T, us, cta_of_tile((long long)us * tiles, T, a.C),
-                          cta_of_tile((long long)us * tiles + tiles - 1, T, a.C), at % kRowsPerCta, lane, M, wsum, acc);
+    for (int q = 0; q < kAtOnce; ++q) {
+      const int r = first + q * kCombineWarps;
+      w[q].n_shared = 0;
+      w[q].c_shared = w[q].r_shared = 0;
+      w[q].slot_shared = 0;
+      if (MODE == kModeShared) {
+        const int3 sh = s_shared[(q0 + q) * kCombineWarps + warp];
+        w[q].n_shared = sh.z - sh.y + 1;
+        w[q].c_shared = sh.y;
+        w[q].r_shared = (b * a.n * G + row0 + r) % kRowsPerCta;
+        w[q].slot_shared = (size_t)sh.y + sh.x;
+      }
+      w[q].c_own = c_first;
+      w[q].r_own = r;
+      w[q].slot_own = (size_t)c_first + geom_unit<MODE>(a, sb, hr);
+      w[q].count = r < valid ? w[q].n_shared + c_last - c_first + 1 : 0;
     }
-    combine_pieces<D>(p, T, geom_unit<MODE>(a, sb, hr), c_first, c_last, r, lane, M, wsum, acc);
-    const int i = row / G, h = g * G + row % G;
-    __nv_bfloat16* dst = p.out + (((size_t)b * a.n + i) * p.Hq + h) * D + lane * DPL;
-    const float inv = wsum > 0.f ? 1.f / wsum : 0.f;
+    combine_pieces<D, kAtOnce, kChunk>(p, T, w, lane, wsum, acc);
 #pragma unroll
-    for (int t = 0; t < DPL; t += 2)
-      *reinterpret_cast<__nv_bfloat162*>(dst + t) = __floats2bfloat162_rn(acc[t] * inv, acc[t + 1] * inv);
+    for (int q = 0; q < kAtOnce; ++q) {
+      const int r = first + q * kCombineWarps;
+      if (r >= valid) break;
+      const int row = row0 + r, i = row / G, h = g * G + row % G;
+      __nv_bfloat16* dst = p.out + (((size_t)b * a.n + i) * p.Hq + h) * D + lane * DPL;
+      const float inv = wsum[q] > 0.f ? 1.f / wsum[q] : 0.f;
+#pragma unroll
+      for (int t = 0; t < DPL; t += 2)
+        *reinterpret_cast<__nv_bfloat162*>(dst + t) = __floats2bfloat162_rn(acc[q][t] * inv, acc[q][t + 1] * inv);
+    }
   }
 }
 
