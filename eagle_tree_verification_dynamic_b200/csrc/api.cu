@@ -165,13 +165,13 @@ size_t eagle_tree_attention_workspace_bytes(int B, int n, int Hq, int Hkv, int D
 size_t eagle_tree_attention_sinks_workspace_bytes(int B, int n, int Hq, int Hkv, int D, int Lmax, int window,
                                                   int sinks) {
   if (B <= 0 || n <= 0 || Hq <= 0 || Hkv <= 0 || D <= 0 || Lmax < 0 || sinks < 0) return 0;
-  return attention_ws_bytes({B, n, Hq, Hkv, D, Lmax, window, sinks, 0});
+  return attention_ws_bytes({B, n, Hq, Hkv, D, Lmax, window, sinks, 0, false});
 }
 
 size_t eagle_tree_attention_shared_workspace_bytes(int B, int n, int Hq, int Hkv, int D, int Lshared, int Lmax) {
   if (B <= 0 || n <= 0 || Hq <= 0 || Hkv <= 0 || D <= 0 || Lshared < 0 || Lmax < 0) return 0;
-  if ((long long)B * n * (Hq / Hkv) > 0x7fffffffLL - kAttnRowsPerUnit) return 0;
-  return attention_ws_bytes({B, n, Hq, Hkv, D, Lmax, 0, 0, Lshared});
+  if ((long long)B * n * (Hq / Hkv) > 0x7fffffffLL - kAttnRowsShared) return 0;
+  return attention_ws_bytes({B, n, Hq, Hkv, D, Lmax, 0, 0, Lshared, true});
 }
 
 }  // extern "C"
@@ -210,13 +210,13 @@ eagle_status attention(AttnCall k, size_t workspace_bytes, void* stream) {
   if (k.Hq % k.Hkv != 0) return EAGLE_ERR_SHAPE;
   if (k.D != 64 && k.D != 128) return EAGLE_ERR_LIMIT;
   if (k.n > EAGLE_MAX_NODES) return EAGLE_ERR_LIMIT;
-  if (shared && (long long)k.B * k.n * (k.Hq / k.Hkv) > 0x7fffffffLL - kAttnRowsPerUnit) return EAGLE_ERR_LIMIT;
+  if (shared && (long long)k.B * k.n * (k.Hq / k.Hkv) > 0x7fffffffLL - kAttnRowsShared) return EAGLE_ERR_LIMIT;
   if (!aligned16(k.q) || !aligned16(k.kt) || !aligned16(k.vt) || !aligned16(k.out) ||
       (k.Lmax > 0 && (!aligned16(k.kc) || !aligned16(k.vc))) ||
       (shared && !paged && k.Lshared > 0 && (!aligned16(k.ks) || !aligned16(k.vs))))
     return EAGLE_ERR_ALIGN;
   const eagle_status st = check_ws(k.ws, workspace_bytes,
-                                   attention_ws_bytes({k.B, k.n, k.Hq, k.Hkv, k.D, k.Lmax, k.window, k.sinks, k.Lshared}));
+                                   attention_ws_bytes({k.B, k.n, k.Hq, k.Hkv, k.D, k.Lmax, k.window, k.sinks, k.Lshared, shared}));
   if (st != EAGLE_OK) return st;
   if (!(k.scale > 0.f)) k.scale = 1.0f / sqrtf((float)k.D);
   return cuda_status(launch_tree_attention(k, static_cast<cudaStream_t>(stream)));

@@ -31,9 +31,10 @@
 //               bf16 over the S it has read.  At the end of a unit's piece the
 //               pair exchanges (max, sum) through shared memory, merges O_A and
 //               O_B, and writes the output or partial
-// Over a shared prefix (wide tiles, 352 threads) the softmax warps of a quarter
-// take whole tiles in turn, O_A over the CTA's even tiles and O_B over its odd
-// ones, and warp 10 issues the O products while warp 1 issues the S ones.
+// Over a shared prefix (wide units, 352 threads) a unit has 256 rows, the two
+// softmax warps of a quarter each have a row block of 128 to themselves, with all
+// keys, Q buffer and O, and warp 10 issues the O products while warp 1 issues the
+// S ones.
 //
 // Every mbarrier wait is bounded (about 2 s of wall time); a timeout sets an
 // abort flag that ends all roles, records a per-CTA status word and still
@@ -51,9 +52,9 @@ namespace eagle {
 using namespace sm100;
 
 constexpr int kTcThreads = 320;   // 10 warps: producer, MMA, 8 softmax
-constexpr int kWideThreads = 352;  // wide tiles: a second MMA warp (the last)
+constexpr int kWideThreads = 352;  // wide units: a second MMA warp (the last)
 constexpr int kBN = kAttnKeysPerTile;
-constexpr int kRowsPerCta = kAttnRowsPerUnit;
+constexpr int kRowsPerCta = kAttnRowsPerUnit;  // rows of one MMA
 constexpr int kMaxStages = 12;
 constexpr int kSmemOptIn = 232448;  // largest dynamic shared memory a block may opt into on sm_100
 constexpr int kCombineThreads = 128;
@@ -61,13 +62,13 @@ constexpr int kCombineThreads = 128;
 // Shared memory from the (1024-byte aligned) dynamic base: a 3 KB header
 // (barriers, then each row's (max, sum) exchange between the two softmax
 // warps of a lane quarter), two Q buffers, the K/V ring (P lives in TMEM).
-// WIDE: how the two softmax warps of a lane quarter share the tiles.  Narrow: each
-// tile's keys in halves (32 per thread), three S buffers; the shortest way from
-// a tile to its product, for CTAs with a handful of tiles.  Wide: whole tiles in
-// turn (64 keys per thread), four S buffers, O_A over the CTA's even tiles and
-// O_B over its odd ones: the waits, the TMEM round trips and the reductions of a
-// tile come once per 64 keys and overlap the other warps' tile, for CTAs that
-// stream many tiles.
+// WIDE: what the two softmax warps of a lane quarter do.  Narrow: a unit has 128
+// rows and they share each tile's keys (32 per thread), three S buffers; the
+// shortest way from a tile to its product, for CTAs with a handful of tiles.
+// Wide: a unit has 256 rows, two blocks of 128 (each with a Q buffer, O_A and
+// O_B), and a warp has a row of its block per thread and all 64 keys: every K/V
+// tile staged serves twice the rows, and two S buffers per block let one block's
+// softmax run beside the other's products.
 template <int D, bool WIDE = false>
 struct TcLayout {
   static constexpr int kAtoms = D / 64;               // 128-byte column atoms along D
@@ -99,7 +100,7 @@ struct TcLayout {
   static_assert(kSmemBytes <= kSmemOptIn, "shared memory");
   static_assert(kXchOff + 2 * 128 * 8 <= kHdrBytes, "header");
   static_assert(kColOB + D <= kTmemCols, "TMEM");
-  static_assert(!WIDE || kSBufs % 2 == 0, "a buffer always the same warps'");
+  static_assert(!WIDE || kSBufs % 2 == 0, "a buffer always the same block's");
 };
 
 struct TcBars {
@@ -130,13 +131,25 @@ static_assert(sizeof(TcBars) <= 512, "barrier block");  // kXchOff
 //                they meet), each cut into tiles of 64 from its own start
 //   kModeShared  the prefix is `shared` keys that every sequence of the batch
 //                has in common, then the sequence's own: the shared keys get
-//                units of their own, whose 128 rows are (node, head) pairs of
-//                the whole batch, so they are read once per 128 rows of the
+//                units of their own, whose rows are (node, head) pairs of
+//                the whole batch, so they are read once per 256 rows of the
 //                batch instead of once per sequence.  Every unit leaves
 //                partials there and the combine joins a row's two units.
 // In kModeShared "sequence" 0 of the schedule is the shared range and 1..B the
 // batch; in the other modes sequence b of the schedule is sequence b.
 enum AttnMode { kModePlain = 0, kModeSinks = 1, kModeShared = 2 };
+
+// Wide units (256 rows) over a shared prefix: there a CTA streams a hundred tiles
+// and more, and with 128 rows each the loads alone took 1040 of 1190 us (16
+// sequences over 32763 keys, 80-node trees; 5.5 GB, in part past L2).  256 rows:
+// 850 us; 32 sequences over 4096 keys 197 -> 150, 4 over 2048 with a KV head per
+// query head 48 -> 37.  A batch of 128 rows a head or fewer leaves half of it
+// empty, with little to share.  With sinks every unit has a sequence's rows only:
+// narrow.
+template <int MODE>
+constexpr bool kWideTiles = MODE == kModeShared;
+template <int MODE>
+constexpr int unit_rows = kWideTiles<MODE> ? kAttnRowsShared : kAttnRowsPerUnit;
 
 struct AttnGeom {
   const int32_t* plen;
@@ -316,8 +329,8 @@ struct TcParams {
   const uint64_t* mask;
   const int32_t* pos;
   __nv_bfloat16* out;
-  float* part_o;    // [C + U][128][D] normalised partial outputs
-  float* part_lse;  // [C + U][128]
+  float* part_o;    // [C + U][unit_rows][D] normalised partial outputs
+  float* part_lse;  // [C + U][unit_rows]
   int* cta_status;  // [C]
   AttnGeom geo;
   int Hq;
@@ -362,10 +375,10 @@ struct RowCtx {
 };
 
 template <int MODE>
-__device__ __forceinline__ void row_issue(RowCtx& rc, const Piece& pc, const TcParams& p, int r_local, int lane,
+__device__ __forceinline__ void row_issue(RowCtx& rc, const Piece& pc, const TcParams& p, int r_unit, int lane,
                                           int G) {
   const AttnGeom& a = p.geo;
-  const int r_glob = (pc.hr % geom_rg<MODE>(a, pc.b)) * kRowsPerCta + r_local;
+  const int r_glob = (pc.hr % geom_rg<MODE>(a, pc.b)) * unit_rows<MODE> + r_unit;
   const bool row_ok = r_glob < geom_nodes<MODE>(a, pc.b) * G;
   const int qi = row_ok ? r_glob / G : 0;
   const size_t nb = (size_t)geom_node0<MODE>(a, pc.b);
@@ -478,27 +491,20 @@ __device__ __forceinline__ uint32_t low_bits(int count) {
   return count >= 32 ? 0xffffffffu : (count > 0 ? (1u << count) - 1u : 0u);
 }
 
-// A batch over a shared prefix is bound by the chain S, softmax, P, O of its tiles,
-// a hundred and more a CTA: wide (32 sequences over 4096 shared keys 291 -> 215 us,
-// 16 over 32763 with 80-node trees 1740 -> 1250 us).  With sinks and a window a CTA
-// has few tiles, narrow: 24.5 us either way at one sequence (window 2048),
-// 87 us against 93 wide at 32 sequences.
-template <int MODE>
-constexpr bool kWideTiles = MODE == kModeShared;
-
 // How long a waiting softmax warp or producer lane may sleep per poll (ns):
 // the MMA warp shares a scheduler with two softmax warps, and a warp that
 // polls in a tight loop takes issue slots from it.
 constexpr uint32_t kSoftmaxSleepNs = 300u;
 constexpr uint32_t kProducerSleepNs = 500u;
 
-// The MMA warps over wide tiles: one issues S = Q K^T, the other O += P V.  Each
+// The MMA warps over wide units: one issues S = Q K^T, the other O += P V.  Each
 // goes through its schedule with all lanes and only the issue itself is one
 // lane's, so that addresses and descriptors stay in uniform registers, where the
 // instruction wants them.  A tile costs such a warp some 500 cycles of waits,
 // elections and commits, as much as the tensor pipe needs for it, so one warp
 // doing both was the bound (with no MMA, no softmax and no load at all the tiles
-// still took 0.55 us each).  S(j) goes where P(j - NB) was, once its PV is done.
+// still took 0.55 us each).  They count products: j is row block j & 1 over tile
+// j / 2.  S(j) goes where P(j - NB) was, once its PV is done.
 template <int D, int MODE>
 __device__ __forceinline__ void mma_scores(const AttnGeom& a, TcBars* bars, uint32_t s_base, uint32_t tmem,
                                            volatile int* abort) {
@@ -512,19 +518,26 @@ __device__ __forceinline__ void mma_scores(const AttnGeom& a, TcBars* bars, uint
   cur.init(bars);
   Piece pc;
   int si = -1, rem = 0, st = 0, ph = 0;  // piece, tiles left in it, stage and its parity
-  for (int j = 0; j < total; ++j) {
-    if (rem == 0) {
-      cur.next(a, pc);
-      ++si;
-      rem = __shfl_sync(kFull, pc.te - pc.tb, 0);
-      if (!__all_sync(kFull, mbar_wait(smem_u32(&bars->q_full[si & 1]), (si >> 1) & 1, abort))) break;
+  bool ok = true;
+  for (int j = 0; ok && j < 2 * total; ++j) {
+    const int blk = j & 1;
+    if (blk == 0) {
+      if (rem == 0) {
+        cur.next(a, pc);
+        ++si;
+        rem = __shfl_sync(kFull, pc.te - pc.tb, 0);
+        ok = __all_sync(kFull, mbar_wait(smem_u32(&bars->q_full[0]), si & 1, abort));
+        if (!ok) break;
+      }
+      --rem;
+      ok = __all_sync(kFull, mbar_wait(smem_u32(&bars->full[st]), ph, abort));
+      if (!ok) break;
     }
-    --rem;
     const int jb = j - NB;
-    if (jb >= 0 && !__all_sync(kFull, mbar_wait(smem_u32(&bars->pv_done[j % NB]), (uint32_t)(jb / NB) & 1u, abort))) break;
-    if (!__all_sync(kFull, mbar_wait(smem_u32(&bars->full[st]), ph, abort))) break;
+    if (jb >= 0) ok = __all_sync(kFull, mbar_wait(smem_u32(&bars->pv_done[j % NB]), (uint32_t)(jb / NB) & 1u, abort));
+    if (!ok) break;
     tc_fence_after();
-    const uint64_t da = q_desc + (uint64_t)((si & 1) * (Lay::kQBytes >> 4));
+    const uint64_t da = q_desc + (uint64_t)(blk * (Lay::kQBytes >> 4));
     const uint64_t db = k_desc + (uint64_t)(st * (Lay::kStageBytes >> 4));
     const uint32_t t_s = tmem + Lay::kColS + (uint32_t)((j % NB) * kBN);
     if (elect_one()) {
@@ -533,10 +546,10 @@ __device__ __forceinline__ void mma_scores(const AttnGeom& a, TcBars* bars, uint
         mma_bf16_ss(t_s, da + ((kk / 4) * 16384 + (kk % 4) * 32) / 16,
                     db + ((kk / 4) * Lay::kKVAtomBytes + (kk % 4) * 32) / 16, id_qk, kk > 0);
       mma_commit(smem_u32(&bars->s_full[j % NB]));
-      if (rem == 0) mma_commit(smem_u32(&bars->q_empty[si & 1]));
+      if (rem == 0 && blk == 1) mma_commit(smem_u32(&bars->q_empty[0]));
     }
     __syncwarp();
-    if (++st == S) {
+    if (blk == 1 && ++st == S) {
       st = 0;
       ph ^= 1;
     }
@@ -558,29 +571,32 @@ __device__ __forceinline__ void mma_outputs(const AttnGeom& a, TcBars* bars, uin
   PieceCursor<MODE> cur;
   cur.init(bars);
   Piece pc;
-  int rem = 0, tix = 0, st = 0;  // tiles left in the piece, tile of the piece, stage
-  for (int j = 0; j < total; ++j, ++tix) {
-    if (rem == 0) {
-      cur.next(a, pc);
-      rem = __shfl_sync(kFull, pc.te - pc.tb, 0);
-      tix = 0;
+  int rem = 0, st = 0;  // tiles left in the piece, stage
+  bool first = true;    // of the piece: an accumulator starts there
+  for (int j = 0; j < 2 * total; ++j) {
+    if ((j & 1) == 0) {
+      first = rem == 0;
+      if (first) {
+        cur.next(a, pc);
+        rem = __shfl_sync(kFull, pc.te - pc.tb, 0);
+      }
+      --rem;
     }
-    --rem;
     // (P(j) is there, so S(j) and with it this stage's copies have landed)
     if (!__all_sync(kFull, mbar_wait(smem_u32(&bars->p_full[j % NB][0]), (uint32_t)(j / NB) & 1u, abort))) break;
     tc_fence_after();
     const uint64_t db = v_desc + (uint64_t)(st * (Lay::kStageBytes >> 4));
     const uint32_t t_p = tmem + Lay::kColS + (uint32_t)((j % NB) * kBN);
     const uint32_t t_o = tmem + ((j & 1) ? Lay::kColOB : Lay::kColOA);
-    const uint32_t more = tix >= 2 ? 1u : 0u;  // an accumulator starts at the piece's first even, first odd tile
+    const uint32_t more = first ? 0u : 1u;
     if (elect_one()) {
 #pragma unroll
       for (int kk = 0; kk < 4; ++kk) mma_bf16_ts(t_o, t_p + (uint32_t)(kk * 8), db + kk * 2048 / 16, id_pv, kk ? 1u : more);
-      mma_commit(smem_u32(&bars->empty[st]));
+      if (j & 1) mma_commit(smem_u32(&bars->empty[st]));
       mma_commit(smem_u32(&bars->pv_done[j % NB]));
     }
     __syncwarp();
-    if (++st == S) st = 0;
+    if ((j & 1) && ++st == S) st = 0;
   }
   if (elect_one()) mma_commit(smem_u32(&bars->mma_idle));
   __syncwarp();
@@ -664,7 +680,9 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
   RowCtx src;
   bool s_have = false;
   const int quad = warp & 3;
-  const int r_local = quad * 32 + lane;  // softmax: TMEM lane = row within the unit's 128
+  const int half = (warp - 2) >> 2;      // softmax: half of a tile's keys (wide: row block)
+  const int r_local = quad * 32 + lane;  // softmax: TMEM lane = row within the block's 128
+  const int r_unit = r_local + (kWide ? half * kRowsPerCta : 0);
   if (warp >= 1) {
     const long long T = geom_prefix<MODE>(a, geom_seqs<MODE>(a), lane);
     const long long t0 = (long long)c * T / a.C, t1 = (long long)(c + 1) * T / a.C;
@@ -682,7 +700,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
       // issued before the block barrier, so ahead of the first K/V copies,
       // and consumed only at the piece's first tile: the producer does not
       // wait for them (a load issued behind the K/V stream waits microseconds)
-      if (s_have && !p.early) row_issue<MODE>(src, spc, p, r_local, lane, G);
+      if (s_have && !p.early) row_issue<MODE>(src, spc, p, r_unit, lane, G);
     }
   }
   // a thread lets the next kernel start only after its own griddep_wait, so
@@ -702,29 +720,33 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
     int si = 0, jg = 0;  // pieces whose Q was loaded; tiles issued
     bool ok = true;
     while (ok && cur.next(a, pc)) {
-      const int qb = si & 1;
+      // narrow: two Q buffers in turn; wide: both hold the piece's 256 rows
+      const int qb = kWide ? 0 : si & 1, qround = kWide ? si : si >> 1;
       const int RG = geom_rg<MODE>(a, pc.b);
       const int g = pc.hr / RG, rg = pc.hr % RG;
       const int node0 = geom_node0<MODE>(a, pc.b), rows = geom_nodes<MODE>(a, pc.b) * G;
-      // Q buffer qb was last read by the QK^T of piece si - 2
-      if (si >= 2 && !__all_sync(kFull, mbar_wait(smem_u32(&bars->q_empty[qb]), ((si >> 1) - 1) & 1, abort))) {
+      // Q buffer qb was last read by the QK^T of piece si - 2 (wide: si - 1)
+      if (qround >= 1 && !__all_sync(kFull, mbar_wait(smem_u32(&bars->q_empty[qb]), (qround - 1) & 1, abort))) {
         ok = false;
         break;
       }
       const uint32_t qdst = s_base + Lay::kQOff + qb * Lay::kQBytes;
       const uint32_t qbar = smem_u32(&bars->q_full[qb]);
       if (p.q_by_tma) {
-        // the 128 rows = (node, head-in-group) pairs: a box of {64 dims, G
+        // 128 rows = (node, head-in-group) pairs: a box of {64 dims, G
         // heads, 128/G nodes} of q viewed as [B*n][Hq][D]
         if (lane == 0) {
-          mbar_arrive_expect_tx(qbar, Lay::kQBytes);
+          constexpr int kBlocks = unit_rows<MODE> / kRowsPerCta;
+          mbar_arrive_expect_tx(qbar, kBlocks * Lay::kQBytes);
           const int rows_i = kRowsPerCta / G;
-          for (int at = 0; at < Lay::kAtoms; ++at)
-            tma_load_3d(qdst + at * 16384, &tm_q, at * 64, g * G, node0 + rg * rows_i, qbar);
+          for (int blk = 0; blk < kBlocks; ++blk)
+            for (int at = 0; at < Lay::kAtoms; ++at)
+              tma_load_3d(qdst + blk * Lay::kQBytes + at * 16384, &tm_q, at * 64, g * G,
+                          node0 + (rg * kBlocks + blk) * rows_i, qbar);
         }
       } else {
-        // gather: 16-byte pieces of the 128 rows into the swizzled K-major tile
-        constexpr int kVec = 128 * Lay::kAtoms * 8;
+        // gather: 16-byte pieces of the unit's rows into the swizzled K-major tiles
+        constexpr int kVec = unit_rows<MODE> * Lay::kAtoms * 8;
         constexpr int kBatch = 8;
         for (int e0 = lane; e0 < kVec; e0 += 32 * kBatch) {
           uint4 v[kBatch];
@@ -734,7 +756,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
             v[u] = make_uint4(0, 0, 0, 0);
             if (e < kVec) {
               const int r = e / (Lay::kAtoms * 8), at = (e / 8) % Lay::kAtoms, cc = e % 8;
-              const int rr = rg * kRowsPerCta + r;
+              const int rr = rg * unit_rows<MODE> + r;
               if (rr < rows) {
                 const int i = rr / G, h = g * G + rr % G;
                 v[u] = *reinterpret_cast<const uint4*>(p.q + (((size_t)node0 + i) * p.Hq + h) * D + at * 64 +
@@ -747,8 +769,8 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
             const int e = e0 + u * 32;
             if (e < kVec) {
               const int r = e / (Lay::kAtoms * 8), at = (e / 8) % Lay::kAtoms, cc = e % 8;
-              *reinterpret_cast<uint4*>(smem + Lay::kQOff + qb * Lay::kQBytes + at * 16384 + r * 128 +
-                                        ((cc ^ (r & 7)) << 4)) = v[u];
+              *reinterpret_cast<uint4*>(smem + Lay::kQOff + (qb + r / kRowsPerCta) * Lay::kQBytes + at * 16384 +
+                                        (r % kRowsPerCta) * 128 + ((cc ^ (r & 7)) << 4)) = v[u];
             }
           }
         }
@@ -802,8 +824,9 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
     if (lane == 0) {
       for (int j = (jg > S ? jg - S : 0); j < jg; ++j)
         mbar_wait_drain(smem_u32(&bars->full[j % S]), (j / S) & 1, 200000000ull);
-      for (int s2 = (si > 2 ? si - 2 : 0); s2 < si; ++s2)
-        mbar_wait_drain(smem_u32(&bars->q_full[s2 & 1]), (s2 >> 1) & 1, 200000000ull);
+      constexpr int kQs = kWide ? 1 : 2;  // Q loads that may be in flight
+      for (int s2 = (si > kQs ? si - kQs : 0); s2 < si; ++s2)
+        mbar_wait_drain(smem_u32(&bars->q_full[s2 % kQs]), (s2 / kQs) & 1, 200000000ull);
     }
   } else if (warp == 1) {
     // ----------------------------------------------------------------- MMA
@@ -925,7 +948,6 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
     // keys of every tile, and which O accumulator, this warp owns.  The two
     // halves keep independent running maxima and sums and are merged once
     // per piece.
-    const int half = (warp - 2) >> 2;
     const uint32_t lane_base = (uint32_t)(quad * 32) << 16;
     constexpr int KW = kWide ? 64 : 32;  // keys per thread and tile
     const uint32_t t_s = tmem + lane_base + Lay::kColS + (uint32_t)(kWide ? 0 : half * 32);
@@ -936,7 +958,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
     if (p.early) {
       griddep_wait();  // mask and pos come from the previous kernel
       griddep_launch_dependents();
-      if (s_have) row_issue<MODE>(src, spc, p, r_local, lane, G);
+      if (s_have) row_issue<MODE>(src, spc, p, r_unit, lane, G);
     }
     Piece pc = spc;
     RowCtx rc = src;
@@ -950,11 +972,11 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
       Piece pn;
       RowCtx rn;
       const bool have_next = scur.next(a, pn);
-      if (have_next) row_issue<MODE>(rn, pn, p, r_local, lane, G);  // in flight during this piece
+      if (have_next) row_issue<MODE>(rn, pn, p, r_unit, lane, G);  // in flight during this piece
       const int RG = geom_rg<MODE>(a, pc.b);
       const int g = pc.hr / RG, rg = pc.hr % RG;
       const int rows = geom_nodes<MODE>(a, pc.b) * G;
-      const int row0 = rg * kRowsPerCta;
+      const int row0 = rg * unit_rows<MODE> + (kWide ? half * kRowsPerCta : 0);
       const int r_glob = row0 + r_local;
       const bool row_ok = r_glob < rows;
       const bool warp_live = row0 + quad * 32 < rows;  // a warp of padding rows only keeps the protocol
@@ -963,18 +985,18 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
       const int win_lo = rc.qpos - a.window + 1;
       float m_used = -INFINITY, l = 0.f;  // reference max (scaled, log2) and row sum of this half
       for (int t = pc.tb; t < pc.te; ++t, ++jg) {
-        // Wide: even tiles of the CTA are the first four warps', odd ones the
-        // others'.  (With an even number of S buffers a buffer is always the same
-        // warps', which so wait for each phase of its barrier in turn: a parity
-        // wait that skips a phase would pass too early.)
-        if (kWide && (jg & 1) != half) continue;
-        const int sbuf = jg % NB;
-        if (!__all_sync(kFull, mbar_wait(smem_u32(&bars->s_full[sbuf]), (uint32_t)(jg / NB) & 1u, abort, 2000000000ull,
+        // jp counts products: wide, two of them (row blocks) per tile.  (An even
+        // number of S buffers: a buffer is always the same warps', which so wait for
+        // each phase of its barrier in turn; a parity wait that skips a phase would
+        // pass too early.)
+        const int jp = kWide ? 2 * jg + half : jg;
+        const int sbuf = jp % NB;
+        if (!__all_sync(kFull, mbar_wait(smem_u32(&bars->s_full[sbuf]), (uint32_t)(jp / NB) & 1u, abort, 2000000000ull,
                                          kSoftmaxSleepNs))) {
           ok = false;
           break;
         }
-        // (wide tiles have no window: all but a range's last tile and the tree's are seen whole by every row)
+        // (wide units have no window: all but a range's last tile and the tree's are seen whole by every row)
         const bool whole_tile = kWide && t < pc.ptiles && piece_key0<MODE>(pc, t) + kBN <= pc.L;
         if (MODE != kModePlain && !whole_tile) {
           // Values of keys that no row sees (past the prefix, between sinks and
@@ -1062,8 +1084,8 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
           const bool rebase = mx > m_used + 8.f;
           if (__any_sync(kFull, rebase && t > pc.tb && l > 0.f)) {
             // these warps' O may only be rescaled once the PV before has finished
-            // accumulating into it (wide: that of two tiles ago)
-            const int jb = jg - (kWide ? 2 : 1);
+            // accumulating into it
+            const int jb = jp - (kWide ? 2 : 1);
             if (!__all_sync(kFull, mbar_wait(smem_u32(&bars->pv_done[jb % NB]), (uint32_t)(jb / NB) & 1u, abort))) {
               ok = false;
               break;
@@ -1114,15 +1136,34 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
       // ---- end of the piece: merge the two halves' (max, sum), normalise,
       // write bf16 output or the partial + log-sum-exp.  Each warp of the pair
       // writes its half of the output columns from both accumulators.
-      if (warp_live) {
-        const int jl = jg - 1;
-        // (wide, the last tile not these warps': S of it first, which was issued
-        // once PV(jl - NB) was done, so that the wait below is for this phase)
-        if (kWide && (jl & 1) != half &&
-            !__all_sync(kFull, mbar_wait(smem_u32(&bars->s_full[jl % NB]), (uint32_t)(jl / NB) & 1u, abort))) {
-          ok = false;
-          break;
+      if (kWide) {
+        // The block's rows are these warps' alone, and their next P only follows
+        // the last read here: no exchange.
+        if (warp_live) {
+          const int jl = 2 * (jg - 1) + half;
+          if (!__all_sync(kFull, mbar_wait(smem_u32(&bars->pv_done[jl % NB]), (uint32_t)(jl / NB) & 1u, abort))) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const float inv = l > 0.f ? 1.f / l : 0.f;
+          const size_t row = ((size_t)c + (size_t)geom_unit<MODE>(a, pc.b, pc.hr)) * unit_rows<MODE> + r_unit;
+          for (int c0 = 0; c0 < D; c0 += 16) {
+            float o[16];
+            tmem_ld16(t_own + c0, o);
+            tmem_wait_ld();
+            if (!row_ok) continue;
+#pragma unroll
+            for (int u = 0; u < 16; ++u) o[u] *= inv;
+            // (whole 32-byte sectors: every piece comes this way)
+            st_global_32(p.part_o + row * D + c0, o);
+            st_global_32(p.part_o + row * D + c0 + 8, o + 8);
+          }
+          if (row_ok) p.part_lse[row] = l > 0.f ? (m_used + __log2f(l)) * (float)kLn2 : -INFINITY;
+          tc_fence_before();
         }
+      } else if (warp_live) {
+        const int jl = jg - 1;
         if (!__all_sync(kFull, mbar_wait(smem_u32(&bars->pv_done[jl % NB]), (uint32_t)(jl / NB) & 1u, abort))) {
           ok = false;
           break;
@@ -1152,11 +1193,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
           tmem_wait_ld();
           if (!row_ok) continue;
 #pragma unroll
-          for (int u = 0; u < 16; ++u) {
-            // (wide: a piece of one tile wrote only one of them)
-            if (kWide) oa[u] = (fa > 0.f ? oa[u] * fa : 0.f) + (fb > 0.f ? ob[u] * fb : 0.f);
-            else oa[u] = fmaf(oa[u], fa, ob[u] * fb);
-          }
+          for (int u = 0; u < 16; ++u) oa[u] = fmaf(oa[u], fa, ob[u] * fb);
           if (pc.whole) {
             __nv_bfloat16* dst = p.out + (((size_t)geom_node0<MODE>(a, pc.b) + qi) * p.Hq + qh) * D + c0;
 #pragma unroll
@@ -1171,15 +1208,9 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
             }
           } else {
             float* dst = p.part_o + (slot * kRowsPerCta + r_local) * D + c0;
-            if constexpr (kWide) {
-              // (whole 32-byte sectors: every piece comes this way)
-              st_global_32(dst, oa);
-              st_global_32(dst + 8, oa + 8);
-            } else {
 #pragma unroll
-              for (int u = 0; u < 4; ++u)
-                *reinterpret_cast<float4*>(dst + 4 * u) = make_float4(oa[4 * u], oa[4 * u + 1], oa[4 * u + 2], oa[4 * u + 3]);
-            }
+            for (int u = 0; u < 4; ++u)
+              *reinterpret_cast<float4*>(dst + 4 * u) = make_float4(oa[4 * u], oa[4 * u + 1], oa[4 * u + 2], oa[4 * u + 3]);
           }
         }
         if (row_ok && !pc.whole && half == 0)
@@ -1247,7 +1278,7 @@ struct RowPieces {
 };
 
 // Merge ROWS rows' pieces, up to CHUNK of each per round of loads.
-template <int D, int ROWS, int CHUNK>
+template <int D, int UNIT, int ROWS, int CHUNK>
 __device__ __forceinline__ void combine_pieces(const CombParams& p, long long T, const RowPieces (&w)[ROWS], int lane,
                                                float (&wsum)[ROWS], float (&acc)[ROWS][D / 32]) {
   constexpr int DPL = D / 32;  // output dims per lane
@@ -1279,7 +1310,7 @@ __device__ __forceinline__ void combine_pieces(const CombParams& p, long long T,
 #pragma unroll
         for (int t = 0; t < DPL; ++t) v[q][j][t] = 0.f;
         if (!live) continue;
-        const size_t sl = ((sh ? w[q].slot_shared : w[q].slot_own) + at) * kRowsPerCta + (sh ? w[q].r_shared : w[q].r_own);
+        const size_t sl = ((sh ? w[q].slot_shared : w[q].slot_own) + at) * UNIT + (sh ? w[q].r_shared : w[q].r_own);
         ls[q][j] = __ldcg(p.part_lse + sl);
         const float* src = p.part_o + sl * D + lane * DPL;
         if constexpr (DPL == 4) {
@@ -1323,7 +1354,8 @@ attn_combine_kernel(const CombParams p) {
   const int sb = MODE == kModeShared ? b + 1 : b;  // the schedule's sequence
   const int g = hr / a.RG, rg = hr % a.RG;
   const int G = p.Hq / a.Hkv;
-  const int row0 = rg * kRowsPerCta, valid = min(kRowsPerCta, a.n * G - row0);
+  constexpr int kUnit = unit_rows<MODE>;
+  const int row0 = rg * kUnit, valid = min(kUnit, a.n * G - row0);
   constexpr int kRows = combine_rows<MODE>;        // per warp,
   constexpr int kAtOnce = MODE == kModeShared ? 2 : 1;  // as many at a time,
   constexpr int kChunk = MODE == kModePlain ? 8 : 4;   // so many pieces of each
@@ -1354,7 +1386,7 @@ attn_combine_kernel(const CombParams p) {
     }
     if (MODE == kModeShared && lane < kBlockRows) {
       const int tiles = geom_tiles<MODE>(a, 0);
-      const int us = g * a.RGs + (b * a.n * G + row0 + (int)blockIdx.y * kBlockRows + lane) / kRowsPerCta;
+      const int us = g * a.RGs + (b * a.n * G + row0 + (int)blockIdx.y * kBlockRows + lane) / kUnit;
       s_shared[lane] = tiles > 0 ? make_int3(us, cta_of_tile((long long)us * tiles, T, a.C),
                                              cta_of_tile((long long)us * tiles + tiles - 1, T, a.C))
                                  : make_int3(us, 0, -1);
@@ -1394,7 +1426,7 @@ attn_combine_kernel(const CombParams p) {
         const int3 sh = s_shared[(q0 + q) * kCombineWarps + warp];
         w[q].n_shared = sh.z - sh.y + 1;
         w[q].c_shared = sh.y;
-        w[q].r_shared = (b * a.n * G + row0 + r) % kRowsPerCta;
+        w[q].r_shared = (b * a.n * G + row0 + r) % kUnit;
         w[q].slot_shared = (size_t)sh.y + sh.x;
       }
       w[q].c_own = c_first;
@@ -1402,7 +1434,7 @@ attn_combine_kernel(const CombParams p) {
       w[q].slot_own = (size_t)c_first + geom_unit<MODE>(a, sb, hr);
       w[q].count = r < valid ? w[q].n_shared + c_last - c_first + 1 : 0;
     }
-    combine_pieces<D, kAtOnce, kChunk>(p, T, w, lane, wsum, acc);
+    combine_pieces<D, unit_rows<MODE>, kAtOnce, kChunk>(p, T, w, lane, wsum, acc);
 #pragma unroll
     for (int q = 0; q < kAtOnce; ++q) {
       const int r = first + q * kCombineWarps;
@@ -1496,7 +1528,7 @@ static cudaError_t launch_tc(const AttnCall& k, cudaStream_t s) {
     const cuuint32_t box[3] = {64, (cuuint32_t)(q_tma ? G : 1), (cuuint32_t)(q_tma ? kRowsPerCta / G : 1)};
     if (!make_map(&mq, k.q, 3, dims, str, box)) return cudaErrorInvalidValue;
   }
-  const AttnShape shape = {B, n, Hq, Hkv, D, Lmax, k.window, k.sinks, k.Lshared};
+  const AttnShape shape = {B, n, Hq, Hkv, D, Lmax, k.window, k.sinks, k.Lshared, MODE == kModeShared};
   const AttnWorkspace wl = attention_ws_layout(shape);
   unsigned char* wsb = static_cast<unsigned char*>(k.ws);
   TcParams p;
@@ -1510,7 +1542,7 @@ static cudaError_t launch_tc(const AttnCall& k, cudaStream_t s) {
   p.geo.plen = k.plen;
   p.geo.B = B;
   p.geo.Hkv = Hkv;
-  p.geo.RG = attention_row_groups(n, Hq, Hkv);
+  p.geo.RG = attention_row_groups(shape);
   p.geo.n = n;
   p.geo.Lmax = Lmax;
   p.geo.window = k.window;
@@ -1559,7 +1591,10 @@ static cudaError_t launch_tc(const AttnCall& k, cudaStream_t s) {
   cp.geo = p.geo;
   cp.Hq = Hq;
   cudaLaunchConfig_t cfg2 = {};
-  cfg2.gridDim = dim3((unsigned)((size_t)B * Hkv * p.geo.RG), kRowsPerCta / kCombineWarps / combine_rows<MODE>);
+  // (over a shared prefix, whose units are often half empty, no blocks for rows that no unit has)
+  constexpr int kPerBlock = kCombineWarps * combine_rows<MODE>;
+  const int rows = MODE == kModeShared && n * G < unit_rows<MODE> ? n * G : unit_rows<MODE>;
+  cfg2.gridDim = dim3((unsigned)((size_t)B * Hkv * p.geo.RG), (rows + kPerBlock - 1) / kPerBlock);
   cfg2.blockDim = dim3(kCombineThreads);
   cfg2.dynamicSmemBytes = 0;
   cfg2.stream = s;

@@ -98,16 +98,16 @@ cudaError_t launch_tree_mask(const int32_t* parents, const int32_t* depth, const
 
 // ---- attention (attention.cu: workspace plan; attention_tc.cu: kernels)
 constexpr int kAttnRowsPerUnit = 128;  // query rows per unit (one MMA M)
+constexpr int kAttnRowsShared = 256;   // over a shared prefix (two)
 constexpr int kAttnKeysPerTile = 64;
 // Workspace of eagle_tree_attention, byte offsets from its (256-aligned) base.
 struct AttnWorkspace {
   size_t status_off;      // int: the device status word (written by every launch)
   size_t cta_status_off;  // int [C]: per-CTA status of the main kernel
-  size_t part_lse_off;    // float [C + U][128]: log-sum-exp of each partial
-  size_t part_o_off;      // float [C + U][128][D]: normalised partial outputs
+  size_t part_lse_off;    // float [C + U][rows per unit]: log-sum-exp of each partial
+  size_t part_o_off;      // float [C + U][rows per unit][D]: normalised partial outputs
   size_t bytes;
 };
-int attention_row_groups(int n, int Hq, int Hkv);
 // The wait probe's limit for the next attention launches (0: off); see
 // eagle_debug_attention_wait_probe.
 unsigned long long attention_wait_probe_ns();
@@ -116,7 +116,10 @@ struct AttnShape {
   int B, n, Hq, Hkv, D, Lmax, window;
   int sinks;    // first keys that stay visible under the window (0: none)
   int Lshared;  // capacity of the prefix that the batch shares (0: none)
+  bool shared;  // the attention over a shared prefix
+  int unit_rows() const { return shared ? kAttnRowsShared : kAttnRowsPerUnit; }
 };
+int attention_row_groups(const AttnShape& a);          // row groups of a sequence
 int attention_shared_row_groups(const AttnShape& a);  // row groups of the whole batch (0 without shared keys)
 int attention_ctas(const AttnShape& a);                // C
 AttnWorkspace attention_ws_layout(const AttnShape& a);

@@ -272,7 +272,7 @@ EAGLE_API eagle_status eagle_tree_attention_paged_with_sinks(
  * The result equals attention over the concatenated prefix up to the order of
  * floating-point sums.  Everything else as in eagle_tree_attention[_paged];
  * the device status word covers the shared pages as well.  Limit: B * n *
- * (Hq / Hkv) < 2^31 - 128.  Workspace: eagle_tree_attention_shared_workspace_bytes
+ * (Hq / Hkv) < 2^31 - 256.  Workspace: eagle_tree_attention_shared_workspace_bytes
  * (paged: Lshared = shared_pages * page_size, Lmax = pages_per_seq * page_size). */
 EAGLE_API size_t eagle_tree_attention_shared_workspace_bytes(int B, int n, int Hq, int Hkv, int D, int Lshared,
                                                              int Lmax);
