@@ -1154,7 +1154,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
             tmem_wait_ld();
             if (!row_ok) continue;
 #pragma unroll
-            for (int u = 0; u < 16; ++u) o[u] *= inv;
+            for (int u = 0; u < 16; ++u) o[u] = inv > 0.f ? o[u] * inv : 0.f;  // (a row that saw nothing: 0, whatever O holds)
             // (whole 32-byte sectors: every piece comes this way)
             st_global_32(p.part_o + row * D + c0, o);
             st_global_32(p.part_o + row * D + c0 + 8, o + 8);
