@@ -143,9 +143,10 @@ enum AttnMode { kModePlain = 0, kModeSinks = 1, kModeShared = 2 };
 // and more, and with 128 rows each the loads alone took 1040 of 1190 us (16
 // sequences over 32763 keys, 80-node trees; 5.5 GB, in part past L2).  256 rows:
 // 850 us; 32 sequences over 4096 keys 197 -> 150, 4 over 2048 with a KV head per
-// query head 48 -> 37.  A batch of 128 rows a head or fewer leaves half of it
-// empty, with little to share.  With sinks every unit has a sequence's rows only:
-// narrow.
+// query head 48 -> 37, 16 over 2048 with 80-node trees 133 -> 114.  A batch of few
+// rows a head leaves half a unit empty and loses a little: 1 of 128 rows over
+// 32768 keys 75 -> 79, 8 of 32 rows over 8192 keys 35 -> 41.  With sinks every unit
+// has one sequence's rows only: narrow.
 template <int MODE>
 constexpr bool kWideTiles = MODE == kModeShared;
 template <int MODE>
@@ -1154,7 +1155,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
             tmem_wait_ld();
             if (!row_ok) continue;
 #pragma unroll
-            for (int u = 0; u < 16; ++u) o[u] = inv > 0.f ? o[u] * inv : 0.f;  // (a row that saw nothing: 0, whatever O holds)
+            for (int u = 0; u < 16; ++u) o[u] = inv > 0.f ? o[u] * inv : 0.f;  // (a row that saw nothing: zeros)
             // (whole 32-byte sectors: every piece comes this way)
             st_global_32(p.part_o + row * D + c0, o);
             st_global_32(p.part_o + row * D + c0 + 8, o + 8);

@@ -238,6 +238,7 @@ EAGLE_API eagle_status eagle_tree_attention_paged(const void* q, const void* k_p
  * sinks > 0 and a window, entries that no node sees (between the sinks and the
  * window, past prefix_len) may hold anything, NaN included, and a paged
  * cache's pages that hold only such keys may be missing from the block table.
+ * Entries that some node sees have to be finite: to the others they count 0 x value.
  * sinks < 0 returns EAGLE_ERR_SHAPE; otherwise as the calls without sinks.
  * Workspace: eagle_tree_attention_sinks_workspace_bytes (paged: Lmax =
  * pages_per_seq * page_size). */
@@ -269,6 +270,7 @@ EAGLE_API eagle_status eagle_tree_attention_paged_with_sinks(
  * shared_table[p / page_size]; a sequence's own keys start on a page of its
  * own (block_table as in eagle_tree_attention_paged).
  * Entries past *shared_len and prefix_len[b] may hold anything.  No window.
+ * Entries that some node sees have to be finite: to the others they count 0 x value.
  * The result equals attention over the concatenated prefix up to the order of
  * floating-point sums.  Everything else as in eagle_tree_attention[_paged];
  * the device status word covers the shared pages as well.  Limit: B * n *

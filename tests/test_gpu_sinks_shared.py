@@ -252,6 +252,15 @@ def test_many_sequences_and_pieces(B, n, Hq, Hkv, D, Ls, top):
         c.check(et.tree_attention_shared(c.q, c.ks, c.vs, c.slen, c.kc, c.vc, c.plen, c.kt, c.vt, c.mask))
 
 
+@pytest.mark.parametrize("B,n,Hq,Hkv,D,Ls,lens", [(40, 100, 12, 3, 64, 1500, 70), (12, 128, 8, 2, 128, 2100, 5),
+                                                  (1, 65, 8, 2, 128, 4000, 65), (7, 43, 6, 2, 128, 700, 130)])
+def test_row_blocks_full_and_in_part(B, n, Hq, Hkv, D, Ls, lens):
+    """More rows a sequence than one unit holds, a last unit with a few rows of its second block or none, pieces longer
+    than the ring."""
+    c = Case(16, B, n, Hq, Hkv, D, np.random.default_rng(4).integers(0, lens, B), Lmax=lens, Ls=Ls)
+    c.check(et.tree_attention_shared(c.q, c.ks, c.vs, c.slen, c.kc, c.vc, c.plen, c.kt, c.vt, c.mask))
+
+
 def test_attention_refusals():
     c = Case(16, 2, 6, 4, 2, 64, [20, 9], Ls=30)
     good = [c.q, c.ks, c.vs, c.slen, c.kc, c.vc, c.plen, c.kt, c.vt, c.mask]
