@@ -590,8 +590,8 @@ __device__ __forceinline__ u64 cta_exclusive(SmpShared& sm, u64 mine, u64* all) 
 // The first bin (in descending order of value) at which the running measure of
 // the cluster reaches `need`; per bin `of(j)`, per CTA the measure `seg` of its
 // segment, `mine` this thread's part of it.  A warp's bins are [j0, j1), its lanes
-// take them in turn.  One thread of the cluster calls found(bin, measure before
-// it) if need is reached.
+// take them in turn.  1 <= need <= the total, so that exactly one thread of the
+// cluster calls found(bin, measure before it): what it says is what all hear next.
 template <typename O, typename F>
 __device__ __forceinline__ void find_bin(Team& tm, const u64* seg, u64 need, u64 mine, int j0, int j1, O&& of,
                                          F&& found) {
@@ -881,14 +881,17 @@ __device__ __forceinline__ bool cut_by_bins(Team& tm, const RowSlice<T>& sl, con
     // ---- fp32: exact sums and a list around the cut, in a second pass
     auto count_of = [&](int j, uint32_t c) { return j < kLastBin ? (u64)c : 0ull; };
     // a bin's weight, estimated: its tokens at their mean place, and what their
-    // spread adds to the mean of an exponential (variance width^2 / 12)
+    // spread adds to the mean of an exponential (variance width^2 / 12); the top's
+    // bin at least the top's own weight, so that no T makes the total 0
+    const int top_bin = bin_of(__float_as_uint(s.top) >> 16);
     auto guess_of = [&](int j, uint32_t c) {
       if (!c || j == 0 || j >= kLastBin) return 0ull;
       const uint32_t mean = j < kZeroBin ? min(0xffffu, (tm.size == 1 ? tm.lows[slot_of(j)] : tm.lows[kNegative + j - seg0]) / c * 16 + 8) : 0x8000u;
       const float v = bin_value(j, mean);
       const u64 w1 = weight(s, sm.tab, v < s.top ? v : s.top);
       const float wide = (bin_value(j, 0xffffu) - bin_value(j, 0)) * (s.c * (float)kLn2);
-      return (u64)((double)c * (double)w1 * (c > 1 ? 1.0 + (double)fminf(wide * wide, 1.f) / 24.0 : 1.0));
+      const u64 w = (u64)((double)c * (double)w1 * (c > 1 ? 1.0 + (double)fminf(wide * wide, 1.f) / 24.0 : 1.0));
+      return j == top_bin ? umax64(w, 1ull << kWeightBits) : w;
     };
     u64 n = 0, w = 0;
     for (int j = j0 + lane; j < j1; j += 32) {
