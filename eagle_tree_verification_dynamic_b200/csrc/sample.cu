@@ -848,14 +848,16 @@ __device__ __forceinline__ bool cut_by_bins(Team& tm, const RowSlice<T>& sl, con
       s.bin1 = at_floor ? cut_bin : sm.pick_entry;
       s.ties = my_ties;
       // Values below 2^-16 are read as 0, off by at most 2^-16 c of their weight:
-      // that must not show in a sum (2^-32 of it), nor by a cut among them
+      // that must not show in a sum (2^-32 of it), nor in what is kept: no cut or
+      // floor among them, and the top, which min-p and an argmax go by, not one of them
       if (cut_bin > kZeroBin && s.floor <= 0.f && (zero_in == 0 || s.total < zero_in)) zero_in = s.total;
-      if (zero_in || cut_bin == kZeroBin) {
+      const bool among = cut_bin == kZeroBin || (cut_bin > kZeroBin && (fabsf(s.floor) < 0x1p-16f || s.top == 0.f));
+      if (zero_in || among) {
         u64 tiny = 0, unused = 0;
         if (tm.bins[0])
           each<T>(sl, [&](float y, int) { tiny += y != 0.f && fabsf(y) < 0x1p-16f; });
         tm.sums2(tiny, unused);
-        if (tiny && (cut_bin == kZeroBin ||
+        if (tiny && (among ||
                      !((double)tiny * (double)weight(s, sm.tab, 0.f) * (double)s.c * 0x1p-16 <= (double)zero_in * 0x1p-32)))
           return false;
       }

@@ -88,3 +88,68 @@ def test_walk_under_top_p_at_low_temperatures(B, V, n, depth, k, wo):
            rng.choice([0.3, 0.6, 0.93], B).astype(np.float32), np.zeros(B, np.float32))
     differ, near = walks_that_differ(c, prm, wo, run_walk(c, sampling_of(*prm), wo))
     assert differ == 0 and near <= B // 4
+
+
+# ------------------------------------------------- values below 2^-16 (bf16 rows count them as 0 where that cannot show)
+def floor_at(top, T, at):
+    """The fp32 min-p whose floor top + T ln(min_p) is next to `at`, and that floor."""
+    m = np.float32(math.exp((at - top) / T))
+    return m, top + T * math.log(float(m))
+
+
+def near_zero_rows():
+    """(row, T, min_p, u): min-p's floor, or the top, among values below 2^-16 in magnitude."""
+    out = []
+    m, fl = floor_at(5.0, 1.0, 5e-6)
+    assert 0 < fl < 2.0 ** -17
+    out.append((np.array([5.0, 1e-5]), 1.0, m, 0.999))                       # above a floor above 0: kept
+    row = np.full(130, 12.0)
+    row[[0, 129]] = -1.2e-5, 1e-6
+    m, fl = floor_at(12.0, 1.0, -5e-6)
+    assert -1.2e-5 < fl < 0
+    out.append((row, 1.0, m, 0.0))                                           # below a floor below 0: not kept
+    row = np.full(20001, -1.0)
+    row[::2], row[9999] = 0.0, 1e-6
+    out.append((row, 10.0, np.float32(1.0), 0.7))                            # the top alone
+    m, _ = floor_at(0.0, 10.0, -1.0)
+    while 10.0 * math.log(float(m)) > -1.0:
+        m = np.nextafter(m, np.float32(0))
+    row = row.copy()
+    row[9999] = 1e-5                                                         # lifts the floor above -1
+    out.append((row, 10.0, m, 1.0 - 2.0 ** -24))
+    row = row.copy()
+    row[row == 0] = -2e-5                                                    # a top below 0: lets the floor down
+    row[9999] = -1e-5
+    m = np.nextafter(m, np.float32(1))
+    assert 10.0 * math.log(float(m)) > -1.0 > -1e-5 + 10.0 * math.log(float(m))
+    out.append((row, 10.0, m, 1.0 - 2.0 ** -24))
+    return out
+
+
+@pytest.mark.parametrize("copies", [1, 60, 300])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_min_p_among_values_near_zero(dtype, copies):
+    for row, T, m, u in near_zero_rows():
+        host = torch.from_numpy(np.tile(row.astype(np.float32), (copies, 1))).to(DT[dtype])
+        full = lambda v: np.full(copies, v, np.float32)
+        tok, lp = et.sample(host.cuda(), f32(full(u)), sampling_of(full(T), None, None, full(m)))
+        check_rows(host[:1].double().numpy(), [u], [T], None, None, [m], (tok[:1], lp[:1]))
+        assert (tok == tok[0]).all() and (lp == lp[0]).all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_the_argmax_of_a_row_of_values_near_zero(dtype):
+    """A walk that has rejected all draft mass ends at the target's argmax, found among values near 0 too."""
+    V, B = 20001, 3
+    target = np.zeros((B, 2, V), np.float32)
+    for b, at in enumerate((0, 777, V - 1)):
+        target[b, :, at] = 1e-5
+    draft = np.full((B, 1, V), -INF, np.float32)
+    draft[:, 0, 55] = 2.0
+    c = dict(target=torch.from_numpy(target).to(DT[dtype]), draft=torch.from_numpy(draft).to(DT[dtype]),
+             tokens=np.full((B, 1), 55, np.int32), parents=np.zeros((B, 1), np.int32),
+             draft_row=np.tile(np.array([0, -1], np.int32), (B, 1)), lse=np.full((B, 1), 2.0),
+             u=np.full((B, 2, 2), 0.9, np.float32), depth=1)
+    prm = (np.full(B, 10.0, np.float32), np.zeros(B, np.int32), np.ones(B, np.float32), np.zeros(B, np.float32))
+    got = run_walk(c, sampling_of(*prm), True)
+    assert walks_that_differ(c, prm, True, got) == (0, 0) and got[2].tolist() == [0, 777, V - 1]
