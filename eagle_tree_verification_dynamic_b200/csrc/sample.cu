@@ -1144,7 +1144,7 @@ __device__ __forceinline__ void draw_kept(Team& tm, RowSlice<T> sl, RowStat s, d
   select_local<T>(sm, sl, thr, [&](float y, int id) {
                     const float x = canon<T>(s, y);
                     return kept(s, x, id) ? weight(s, sm.tab, x) : 0ull;
-                  }, [&](int id, float y) { hit(id, canon<T>(s, y)); });
+                  }, [&](int id, float y) { hit(id, s.infinite ? 0.f : y); });
 }
 
 // Four CTAs per SM (64 registers): the passes wait on memory and shared atomics in

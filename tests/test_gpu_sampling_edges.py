@@ -137,6 +137,21 @@ def test_min_p_among_values_near_zero(dtype, copies):
         assert (tok == tok[0]).all() and (lp == lp[0]).all()
 
 
+@pytest.mark.parametrize("copies", [1, 300])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_log_probability_of_a_value_near_zero(dtype, copies):
+    """The drawn logit's own value counts, though the row's sums read it as 0."""
+    V = 5001
+    for x in (1.4e-5, -1.4e-5):
+        row = np.full(V, -40.0, np.float32)
+        row[100], row[V - 1] = 12.0, x
+        host = torch.from_numpy(np.tile(row, (copies, 1))).to(DT[dtype])
+        u = np.full(copies, 1.0 - 2.0 ** -24, np.float32)
+        tok, lp = et.sample(host.cuda(), f32(u))
+        check_rows(host[:1].double().numpy(), u, None, None, None, None, (tok[:1], lp[:1]))
+        assert (tok == V - 1).all() and (lp == lp[0]).all()
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_the_argmax_of_a_row_of_values_near_zero(dtype):
     """A walk that has rejected all draft mass ends at the target's argmax, found among values near 0 too."""
