@@ -140,13 +140,16 @@ struct RowStat {
   u64 ties;
 };
 
-// A logit as the passes over the row read it, see RowStat::infinite and merged
-// (filter_row makes sure that no sum notices the latter).
+// A logit's own value (in a row that holds +inf, see RowStat::infinite).
+__device__ __forceinline__ float own(const RowStat& s, float x) {
+  return s.infinite ? (x == INFINITY ? 0.f : -INFINITY) : x;
+}
+// A logit as the passes that have to agree with the bins read it, see
+// RowStat::merged (cut_by_bins makes sure that no sum notices, nor what is kept).
 template <typename T>
 __device__ __forceinline__ float canon(const RowStat& s, float x) {
-  if (s.infinite) return x == INFINITY ? 0.f : -INFINITY;
   if (sizeof(T) == 2 && s.merged) return fabsf(x) < 0x1p-16f ? 0.f : x;
-  return x;
+  return own(s, x);
 }
 
 __device__ __forceinline__ bool kept(const RowStat& s, float x, int id) {
@@ -1144,7 +1147,7 @@ __device__ __forceinline__ void draw_kept(Team& tm, RowSlice<T> sl, RowStat s, d
   select_local<T>(sm, sl, thr, [&](float y, int id) {
                     const float x = canon<T>(s, y);
                     return kept(s, x, id) ? weight(s, sm.tab, x) : 0ull;
-                  }, [&](int id, float y) { hit(id, s.infinite ? 0.f : y); });
+                  }, [&](int id, float y) { hit(id, own(s, y)); });
 }
 
 // Four CTAs per SM (64 registers): the passes wait on memory and shared atomics in
@@ -1262,7 +1265,7 @@ accept_sampling_kernel(const T* __restrict__ tgt, const T* __restrict__ dft, con
       const int x = ws.tok[tid];
       double p = 0.0, q = 0.0;
       if (x >= 0 && x < V && r >= 0) {
-        const float xt = canon<T>(s, (float)trow[x]);
+        const float xt = own(s, (float)trow[x]);
         if (kept(s, xt, x)) p = (double)weight(s, sm.tab, xt) * inv_S;
         q = exp((double)(float)drow[x] - lse);
       }
@@ -1275,7 +1278,7 @@ accept_sampling_kernel(const T* __restrict__ tgt, const T* __restrict__ dft, con
     int moved = 0;
     // max(0, p - t q) of a token
     auto residual = [&](float y, int id) {
-      const float x = canon<T>(s, y);
+      const float x = own(s, y);
       if (!kept(s, x, id)) return 0.0;
       const u64 w = weight(s, sm.tab, x);
       if (w == 0) return 0.0;

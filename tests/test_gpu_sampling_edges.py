@@ -153,6 +153,34 @@ def test_log_probability_of_a_value_near_zero(dtype, copies):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_a_child_is_accepted_by_its_own_value_near_zero(dtype):
+    """p of a drafted token with logit x = +-1.4e-5 differs from that of 0 by 1.4e-5 of it; u between the two."""
+    V, B, at = 1000, 2, 321
+    target = np.full((B, 2, V), -40.0, np.float32)
+    target[:, :, 5] = 12.0
+    target[0, :, at], target[1, :, at] = 1.4e-5, -1.4e-5
+    target = torch.from_numpy(target).to(DT[dtype])
+    draft = np.full((B, 1, V), -40.0, np.float32)
+    draft[:, 0, 5], draft[:, 0, at] = 12.0, 0.6875
+    d = draft[0, 0].astype(np.float64)
+    lse = math.log(np.exp(d - 12.0).sum()) + 12.0
+    q = math.exp(0.6875 - lse)
+    u = np.full((B, 2, 2), 0.25, np.float32)
+    for b in range(B):
+        t = target[b, 0].double().numpy()
+        p = math.exp(t[at]) / np.exp(t).sum()
+        p0 = 1.0 / np.exp(t).sum()                       # were it 0
+        u[b, 0, 1] = (p + p0) / 2 / q
+        assert min(p, p0) < u[b, 0, 1] * q < max(p, p0)
+    c = dict(target=target, draft=torch.from_numpy(draft).to(DT[dtype]), tokens=np.full((B, 1), at, np.int32),
+             parents=np.zeros((B, 1), np.int32), draft_row=np.tile(np.array([0, -1], np.int32), (B, 1)),
+             lse=np.full((B, 1), lse), u=u, depth=1)
+    prm = (np.ones(B, np.float32), np.zeros(B, np.int32), np.ones(B, np.float32), np.zeros(B, np.float32))
+    got = run_walk(c, sampling_of(*prm), False)
+    assert walks_that_differ(c, prm, False, got) == (0, 0) and got[0].tolist() == [1, 0]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_the_argmax_of_a_row_of_values_near_zero(dtype):
     """A walk that has rejected all draft mass ends at the target's argmax, found among values near 0 too."""
     V, B = 20001, 3
