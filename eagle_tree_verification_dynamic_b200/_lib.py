@@ -10,7 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from dataclasses import dataclass
+from dataclasses import dataclass, replace
 from typing import Optional
 
 import torch
@@ -51,6 +51,7 @@ class SamplingStruct(ctypes.Structure):
 
 class StepOptions(ctypes.Structure):
     _fields_ = [("sinks", _c_i), ("sampling", ctypes.POINTER(SamplingStruct))]
+    parameters = None  # the Sampling that `sampling` points into (step_options sets both)
 
 
 class CostTableStruct(ctypes.Structure):
@@ -545,6 +546,8 @@ class Sampling:
 def sample_into(logits, uniforms, sampling: Optional[Sampling], tokens, logprob=None):
     """eagle_sample into preallocated tokens [rows] int32 and logprob [rows] f32 (or None)."""
     rows, V = logits.shape
+    if sampling is not None:
+        sampling.check(rows, logits)
     st = None if sampling is None else ctypes.byref(sampling.struct())
     with _on(logits.device):
         _check(lib().eagle_sample(_ptr(logits), _dtype_code(logits), rows, V, logits.stride(0) if rows > 1 else V, st,
@@ -562,8 +565,6 @@ def sample(logits: torch.Tensor, uniforms: torch.Tensor, sampling: Optional[Samp
     _need_cuda(logits[:0].reshape(-1), uniforms)
     if uniforms.dtype != torch.float32 or uniforms.numel() != rows:
         raise EagleError(f"uniforms must be {rows} x float32")
-    if sampling is not None:
-        sampling.check(rows, logits)
     tokens = torch.empty(rows, dtype=torch.int32, device=logits.device)
     logprob = torch.empty(rows, dtype=torch.float32, device=logits.device)
     sample_into(logits, uniforms, sampling, tokens, logprob)
@@ -578,6 +579,9 @@ def accept_into(target_logits, tokens, parents, draft_row, depth, uniforms, draf
     ddt = _dtype_code(draft_logits) if draft_logits is not None else 0
     rule = SAMPLE_WITHOUT_REPLACEMENT if without_replacement else SAMPLE_WITH_REPLACEMENT
     if sampling is not None:
+        if uniforms is None:
+            raise EagleError("accept: sampling parameters need uniforms")
+        sampling.check(B, target_logits)
         with _on(target_logits.device):
             _check(lib().eagle_accept_with_sampling(
                 _ptr(target_logits), _dtype_code(target_logits), _ptr(draft_logits), ddt, _ptr(draft_lse), R,
@@ -599,10 +603,6 @@ def accept(target_logits, tokens, parents, draft_row, depth: int, uniforms=None,
     distribution under each sequence's temperature, top-k, top-p and min-p (sampled acceptance only)."""
     _need_cuda(target_logits, tokens, parents, draft_row, uniforms, draft_logits, draft_lse)
     B, n1, V = target_logits.shape
-    if sampling is not None:
-        if uniforms is None:
-            raise EagleError("accept: sampling parameters need uniforms")
-        sampling.check(B, target_logits)
     dev = target_logits.device
     acc = torch.empty(B, dtype=torch.int32, device=dev)
     path = torch.empty(B, depth, dtype=torch.int32, device=dev)
@@ -632,8 +632,10 @@ def step_in(draft_logits, target_logits, depth, k, m, q, k_cache, v_cache, prefi
 
 
 def step_options(sinks: int = 0, sampling: Optional[Sampling] = None) -> StepOptions:
-    """The C step's options: a window's sinks and the sequences' sampling parameters."""
-    return StepOptions(sinks, None if sampling is None else ctypes.pointer(sampling.struct()))
+    """The C step's options: a window's sinks and the sequences' sampling parameters (whose tensors they keep alive)."""
+    options = StepOptions(sinks, None if sampling is None else ctypes.pointer(sampling.struct()))
+    options.parameters = None if sampling is None else replace(sampling)
+    return options
 
 
 def step_workspace_bytes(si: StepIn, options: Optional[StepOptions] = None) -> int:
@@ -643,6 +645,8 @@ def step_workspace_bytes(si: StepIn, options: Optional[StepOptions] = None) -> i
 def step_into(si: StepIn, tree: Tree, mask, pos, attn_out, accepted_len, path, bonus, ws: torch.Tensor,
               device, options: Optional[StepOptions] = None) -> int:
     """Enqueue one whole step (build + fused mask, attention, acceptance) on the current stream."""
+    if options is not None and options.parameters is not None:
+        options.parameters.check(si.B, tree.tokens)
     so = StepOut(tree.struct(), _ptr(mask), _ptr(pos), _ptr(attn_out), _ptr(accepted_len), _ptr(path), _ptr(bonus))
     n_out = _c_i(0)
     _check(lib().eagle_verify_step_with_options(ctypes.byref(si), options, ctypes.byref(so), ctypes.byref(n_out),

@@ -103,6 +103,7 @@ class VerifyStep:
 
     def accept(self, target_logits, uniforms: Optional[torch.Tensor], draft_logits,
                sampling: Optional[L.Sampling] = None):
+        self._sampled(sampling)
         if self.s.stochastic:
             L.accept_into(target_logits, self.tree.tokens, self.tree.parents, self.tree.draft_row, self.s.depth,
                           uniforms, draft_logits, self.tree.row_lse, self.accepted_len, self.path, self.bonus,
@@ -111,15 +112,20 @@ class VerifyStep:
             L.accept_into(target_logits, self.tree.tokens, self.tree.parents, self.tree.draft_row, self.s.depth,
                           None, None, None, self.accepted_len, self.path, self.bonus, self.ws_acc)
 
+    def _sampled(self, sampling: Optional[L.Sampling]):
+        if sampling is not None and not self.s.stochastic:
+            raise L.EagleError("sampling parameters need sampled acceptance (stochastic=True)")
+
     def fused(self, inp: dict):
         """The same step as one eagle_verify_step call (same outputs)."""
         s = self.s
+        self._sampled(inp.get("sampling"))
         si = L.step_in(inp["draft_logits"], inp["target_logits"], s.depth, s.k, s.m, inp["q"], inp["k_cache"],
                        inp["v_cache"], inp["prefix_len"], inp["k_tree"], inp["v_tree"],
                        inp.get("uniforms") if s.stochastic else None, s.window,
                        without_replacement=s.without_replacement,
                        block_table=inp["block_table"] if s.paged else None)
-        options = L.step_options(s.sinks, inp.get("sampling") if s.stochastic else None)
+        options = L.step_options(s.sinks, inp.get("sampling"))
         L.step_into(si, self.tree, self.mask, self.pos, self.out, self.accepted_len, self.path, self.bonus,
                     self.ws_step, self.device, options)
         self._step_in, self._step_options = si, options
