@@ -240,8 +240,9 @@ def row_stats_into(logits: torch.Tensor, k: int, tok: torch.Tensor, val: torch.T
     or None) and workspace."""
     rows, V = logits.reshape(-1, logits.shape[-1]).shape
     dt = _dtype_code(logits)
-    _check(lib().eagle_row_stats(_ptr(logits), dt, rows, V, k, _ptr(tok), _ptr(val), _ptr(lse), _ptr(ws),
-                                 ws.numel(), _stream(logits.device)), "eagle_row_stats")
+    with _on(logits.device):
+        _check(lib().eagle_row_stats(_ptr(logits), dt, rows, V, k, _ptr(tok), _ptr(val), _ptr(lse), _ptr(ws),
+                                     ws.numel(), _stream(logits.device)), "eagle_row_stats")
 
 
 def row_stats(logits: torch.Tensor, k: int, want_lse: bool = True):
@@ -255,8 +256,9 @@ def row_stats(logits: torch.Tensor, k: int, want_lse: bool = True):
     dt = _dtype_code(logits)
     nb = lib().eagle_row_stats_workspace_bytes(rows, V, dt, k)
     ws = _workspace(nb, dev)
-    _check(lib().eagle_row_stats(_ptr(logits), dt, rows, V, k, _ptr(tok), _ptr(val), _ptr(lse),
-                                 _ptr(ws), nb, _stream(dev)), "eagle_row_stats")
+    with _on(dev):
+        _check(lib().eagle_row_stats(_ptr(logits), dt, rows, V, k, _ptr(tok), _ptr(val), _ptr(lse),
+                                     _ptr(ws), nb, _stream(dev)), "eagle_row_stats")
     return tok, val, lse
 
 
@@ -301,9 +303,10 @@ def tree_build_into(draft_logits: torch.Tensor, depth: int, k: int, m: int, tree
     dt = _dtype_code(draft_logits)
     st = tree.struct()
     n_out = _c_i(0)
-    _check(lib().eagle_tree_build(_ptr(draft_logits), dt, B, R, V, depth, k, m, ctypes.byref(st),
-                                  ctypes.byref(n_out), _ptr(ws), ws.numel(), _stream(draft_logits.device)),
-           "eagle_tree_build")
+    with _on(draft_logits.device):
+        _check(lib().eagle_tree_build(_ptr(draft_logits), dt, B, R, V, depth, k, m, ctypes.byref(st),
+                                      ctypes.byref(n_out), _ptr(ws), ws.numel(), _stream(draft_logits.device)),
+               "eagle_tree_build")
     return n_out.value
 
 
@@ -320,8 +323,9 @@ def tree_build(draft_logits: torch.Tensor, depth: int, k: int, m: int) -> Tree:
 # ---------------------------------------------------------------- tree mask
 def tree_mask_into(parents, depth, prefix_len, mask, pos):
     B, n = parents.shape
-    _check(lib().eagle_tree_mask(_ptr(parents), _ptr(depth), _ptr(prefix_len), B, n, _ptr(mask), _ptr(pos),
-                                 _stream(parents.device)), "eagle_tree_mask")
+    with _on(parents.device):
+        _check(lib().eagle_tree_mask(_ptr(parents), _ptr(depth), _ptr(prefix_len), B, n, _ptr(mask), _ptr(pos),
+                                     _stream(parents.device)), "eagle_tree_mask")
 
 
 def tree_mask(parents: torch.Tensor, depth: Optional[torch.Tensor] = None,
@@ -496,10 +500,11 @@ def kv_compact_paged_into(k_tree, v_tree, path, accepted_len, prefix_len, k_page
                           new_prefix_len):
     """kv_compact into a paged cache (pools updated in place); new lengths into new_prefix_len."""
     B, n, Hkv, D = k_tree.shape
-    _check(lib().eagle_kv_compact_paged(_ptr(k_tree), _ptr(v_tree), _ptr(path), _ptr(accepted_len), _ptr(prefix_len),
-                                        _ptr(k_pages), _ptr(v_pages), k_pages.shape[0], k_pages.shape[2],
-                                        _ptr(block_table), block_table.shape[1], _ptr(new_prefix_len), B, n, Hkv, D,
-                                        path.shape[1], _stream(k_tree.device)), "eagle_kv_compact_paged")
+    with _on(k_tree.device):
+        _check(lib().eagle_kv_compact_paged(_ptr(k_tree), _ptr(v_tree), _ptr(path), _ptr(accepted_len), _ptr(prefix_len),
+                                            _ptr(k_pages), _ptr(v_pages), k_pages.shape[0], k_pages.shape[2],
+                                            _ptr(block_table), block_table.shape[1], _ptr(new_prefix_len), B, n, Hkv, D,
+                                            path.shape[1], _stream(k_tree.device)), "eagle_kv_compact_paged")
 
 
 def kv_compact_paged(k_tree, v_tree, path, accepted_len, prefix_len, k_pages, v_pages, block_table) -> torch.Tensor:
@@ -589,11 +594,12 @@ def accept_into(target_logits, tokens, parents, draft_row, depth, uniforms, draf
                 n, V, depth, _ptr(accepted_len), _ptr(path), _ptr(bonus), _ptr(ws), ws.numel(),
                 _stream(target_logits.device)), "eagle_accept_with_sampling")
         return
-    _check(lib().eagle_accept_with_rule(_ptr(target_logits), _dtype_code(target_logits), _ptr(draft_logits), ddt,
-                                        _ptr(draft_lse), R, _ptr(tokens), _ptr(parents), _ptr(draft_row),
-                                        _ptr(uniforms), rule, B, n, V, depth, _ptr(accepted_len), _ptr(path),
-                                        _ptr(bonus), _ptr(ws), ws.numel(), _stream(target_logits.device)),
-           "eagle_accept_with_rule")
+    with _on(target_logits.device):
+        _check(lib().eagle_accept_with_rule(_ptr(target_logits), _dtype_code(target_logits), _ptr(draft_logits), ddt,
+                                            _ptr(draft_lse), R, _ptr(tokens), _ptr(parents), _ptr(draft_row),
+                                            _ptr(uniforms), rule, B, n, V, depth, _ptr(accepted_len), _ptr(path),
+                                            _ptr(bonus), _ptr(ws), ws.numel(), _stream(target_logits.device)),
+               "eagle_accept_with_rule")
 
 
 def accept(target_logits, tokens, parents, draft_row, depth: int, uniforms=None, draft_logits=None,
@@ -649,8 +655,9 @@ def step_into(si: StepIn, tree: Tree, mask, pos, attn_out, accepted_len, path, b
         options.parameters.check(si.B, tree.tokens)
     so = StepOut(tree.struct(), _ptr(mask), _ptr(pos), _ptr(attn_out), _ptr(accepted_len), _ptr(path), _ptr(bonus))
     n_out = _c_i(0)
-    _check(lib().eagle_verify_step_with_options(ctypes.byref(si), options, ctypes.byref(so), ctypes.byref(n_out),
-                                                _ptr(ws), ws.numel(), _stream(device)), "eagle_verify_step")
+    with _on(device):
+        _check(lib().eagle_verify_step_with_options(ctypes.byref(si), options, ctypes.byref(so), ctypes.byref(n_out),
+                                                    _ptr(ws), ws.numel(), _stream(device)), "eagle_verify_step")
     return n_out.value
 
 
@@ -665,9 +672,10 @@ def kv_compact_into(k_tree, v_tree, path, accepted_len, prefix_len, k_cache, v_c
     """Append the accepted path's tree keys/values to the caches (in place); new lengths into new_prefix_len."""
     B, n, Hkv, D = k_tree.shape
     Lmax, depth = k_cache.shape[2], path.shape[1]
-    _check(lib().eagle_kv_compact(_ptr(k_tree), _ptr(v_tree), _ptr(path), _ptr(accepted_len), _ptr(prefix_len),
-                                  _ptr(k_cache), _ptr(v_cache), _ptr(new_prefix_len), B, n, Hkv, D, Lmax, depth,
-                                  _stream(k_tree.device)), "eagle_kv_compact")
+    with _on(k_tree.device):
+        _check(lib().eagle_kv_compact(_ptr(k_tree), _ptr(v_tree), _ptr(path), _ptr(accepted_len), _ptr(prefix_len),
+                                      _ptr(k_cache), _ptr(v_cache), _ptr(new_prefix_len), B, n, Hkv, D, Lmax, depth,
+                                      _stream(k_tree.device)), "eagle_kv_compact")
 
 
 def kv_compact(k_tree, v_tree, path, accepted_len, prefix_len, k_cache, v_cache) -> torch.Tensor:
@@ -698,29 +706,33 @@ class TreeGrower:
         self.flogv = torch.empty(B, k, dtype=torch.float64, device=self.device)
 
     def begin(self, root_logits: torch.Tensor):
-        _check(lib().eagle_tree_grow_begin(_ptr(root_logits), self.dt, self.B, self.V, self.depth, self.k,
-                                           _ptr(self.state), self.state.numel(), _ptr(self.ftok), _ptr(self.fpar),
-                                           _stream(self.device)), "eagle_tree_grow_begin")
+        with _on(self.device):
+            _check(lib().eagle_tree_grow_begin(_ptr(root_logits), self.dt, self.B, self.V, self.depth, self.k,
+                                               _ptr(self.state), self.state.numel(), _ptr(self.ftok), _ptr(self.fpar),
+                                               _stream(self.device)), "eagle_tree_grow_begin")
         return self.ftok, self.fpar
 
     def level(self, level_logits: torch.Tensor, level: int):
-        _check(lib().eagle_tree_grow_level(_ptr(level_logits), self.dt, self.B, self.V, self.depth, self.k, level,
-                                           _ptr(self.state), self.state.numel(), _ptr(self.ftok), _ptr(self.fpar),
-                                           _stream(self.device)), "eagle_tree_grow_level")
+        with _on(self.device):
+            _check(lib().eagle_tree_grow_level(_ptr(level_logits), self.dt, self.B, self.V, self.depth, self.k, level,
+                                               _ptr(self.state), self.state.numel(), _ptr(self.ftok), _ptr(self.fpar),
+                                               _stream(self.device)), "eagle_tree_grow_level")
         return self.ftok, self.fpar
 
     def level_width(self, level_logits: torch.Tensor, level: int, width: int):
         """A level drafted from the first `width` frontier slots only: level_logits [B][width][V]."""
-        _check(lib().eagle_tree_grow_level_width(_ptr(level_logits), self.dt, self.B, self.V, self.depth, self.k,
-                                                 level, width, _ptr(self.state), self.state.numel(), _ptr(self.ftok),
-                                                 _ptr(self.fpar), _stream(self.device)), "eagle_tree_grow_level_width")
+        with _on(self.device):
+            _check(lib().eagle_tree_grow_level_width(_ptr(level_logits), self.dt, self.B, self.V, self.depth, self.k,
+                                                     level, width, _ptr(self.state), self.state.numel(), _ptr(self.ftok),
+                                                     _ptr(self.fpar), _stream(self.device)), "eagle_tree_grow_level_width")
         return self.ftok, self.fpar
 
     def frontier_logv(self) -> torch.Tensor:
         """The last level's k best candidates per sequence, log V in rank order [B][k] (device, float64)."""
-        _check(lib().eagle_tree_grow_frontier_logv(self.dt, self.B, self.V, self.depth, self.k, _ptr(self.state),
-                                                   self.state.numel(), _ptr(self.flogv), _stream(self.device)),
-               "eagle_tree_grow_frontier_logv")
+        with _on(self.device):
+            _check(lib().eagle_tree_grow_frontier_logv(self.dt, self.B, self.V, self.depth, self.k, _ptr(self.state),
+                                                       self.state.numel(), _ptr(self.flogv), _stream(self.device)),
+                   "eagle_tree_grow_frontier_logv")
         return self.flogv
 
     def finish_widths(self, widths) -> Tree:
@@ -731,16 +743,18 @@ class TreeGrower:
         tree = alloc_tree(self.B, R, levels, self.k, max(1, sum(int(x) for x in widths)), self.device)
         st = tree.struct()
         n_out = _c_i(0)
-        _check(lib().eagle_tree_grow_finish_widths(self.dt, self.B, self.V, self.depth, self.k, levels, w,
-                                                   _ptr(self.state), self.state.numel(), ctypes.byref(st),
-                                                   ctypes.byref(n_out), _stream(self.device)),
-               "eagle_tree_grow_finish_widths")
+        with _on(self.device):
+            _check(lib().eagle_tree_grow_finish_widths(self.dt, self.B, self.V, self.depth, self.k, levels, w,
+                                                       _ptr(self.state), self.state.numel(), ctypes.byref(st),
+                                                       ctypes.byref(n_out), _stream(self.device)),
+                   "eagle_tree_grow_finish_widths")
         return tree
 
     def gains(self) -> torch.Tensor:
-        _check(lib().eagle_tree_grow_gains(self.dt, self.B, self.V, self.depth, self.k, _ptr(self.state),
-                                           self.state.numel(), _ptr(self.gain), _stream(self.device)),
-               "eagle_tree_grow_gains")
+        with _on(self.device):
+            _check(lib().eagle_tree_grow_gains(self.dt, self.B, self.V, self.depth, self.k, _ptr(self.state),
+                                               self.state.numel(), _ptr(self.gain), _stream(self.device)),
+                   "eagle_tree_grow_gains")
         return self.gain
 
     def finish(self, m: int, levels: Optional[int] = None) -> Tree:
@@ -749,9 +763,10 @@ class TreeGrower:
         tree = alloc_tree(self.B, R, levels, self.k, m, self.device)
         st = tree.struct()
         n_out = _c_i(0)
-        _check(lib().eagle_tree_grow_finish(self.dt, self.B, self.V, self.depth, self.k, levels, m,
-                                            _ptr(self.state), self.state.numel(), ctypes.byref(st),
-                                            ctypes.byref(n_out), _stream(self.device)), "eagle_tree_grow_finish")
+        with _on(self.device):
+            _check(lib().eagle_tree_grow_finish(self.dt, self.B, self.V, self.depth, self.k, levels, m,
+                                                _ptr(self.state), self.state.numel(), ctypes.byref(st),
+                                                ctypes.byref(n_out), _stream(self.device)), "eagle_tree_grow_finish")
         return tree
 
 
@@ -809,6 +824,7 @@ def static_tree_build(draft_logits: torch.Tensor, parents, ranks) -> Tree:
     nb = lib().eagle_static_tree_workspace_bytes(B, V, dt, p, r, n)
     ws = _workspace(max(nb, 256), dev)
     st = tree.struct()
-    _check(lib().eagle_static_tree_build(_ptr(draft_logits), dt, B, R, V, p, r, n, ctypes.byref(st), _ptr(ws),
-                                         ws.numel(), _stream(dev)), "eagle_static_tree_build")
+    with _on(dev):
+        _check(lib().eagle_static_tree_build(_ptr(draft_logits), dt, B, R, V, p, r, n, ctypes.byref(st), _ptr(ws),
+                                             ws.numel(), _stream(dev)), "eagle_static_tree_build")
     return tree

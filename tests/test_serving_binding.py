@@ -93,3 +93,38 @@ def test_greedy_steps_refuse_sampling_parameters(calls):
     assert calls == []
     step.fused(step_inputs(step))
     assert "eagle_verify_step_with_options" in calls
+
+
+def test_every_launch_is_on_its_tensors_device(calls):
+    i32 = lambda *d: torch.zeros(*d, dtype=torch.int32)
+    bf = lambda *d: torch.zeros(*d, dtype=torch.bfloat16)
+    prm = et.Sampling(torch.ones(3), None, torch.ones(3), None)
+    for stochastic in (False, True):
+        step = VerifyStep(StepShape(**SHAPE, stochastic=stochastic), "cpu")
+        inp = step_inputs(step, **({"sampling": prm} if stochastic else {}))
+        step.fused(inp)
+        step(inp)
+        step.draft_sweep(inp["draft_logits"])
+        step.accept_sweep(inp["target_logits"])
+        step.accept(inp["target_logits"], inp["uniforms"], inp["draft_logits"])
+    et.row_stats(torch.zeros(3, 50), 2)
+    et.tree_mask(i32(3, 4), i32(3, 4), i32(3))
+    et.sample_into(torch.zeros(3, 50), torch.zeros(3), prm, i32(3))
+    kt, cache = bf(3, 4, 2, 64), bf(3, 2, 128, 64)
+    et.kv_compact(kt, kt, i32(3, 2), i32(3), i32(3), cache, cache)
+    et.kv_compact_paged(kt, kt, i32(3, 2), i32(3), i32(3), cache, cache, i32(3, 2))
+    pool, mask = bf(8, 2, 64, 64), torch.zeros(3, 4, 2, dtype=torch.int64)
+    q = bf(3, 4, 4, 64)
+    et.tree_attention_paged(q, pool, pool, i32(3, 2), i32(3), kt, kt, mask, check=False)
+    et.tree_attention_shared(q, bf(2, 64, 64), bf(2, 64, 64), i32(1), cache, cache, i32(3), kt, kt, mask, check=False)
+    et.tree_attention_shared_paged(q, pool, pool, i32(2), i32(1), i32(3, 2), i32(3), kt, kt, mask, check=False)
+    et.static_tree_build(torch.zeros(3, 2, 50), [0, 1], [0, 0])
+    g = et.TreeGrower(3, 50, 2, 2, torch.float32, "cpu")
+    g.begin(torch.zeros(3, 50))
+    g.level(torch.zeros(3, 2, 50), 2)
+    g.level_width(torch.zeros(3, 1, 50), 2, 1)
+    g.frontier_logv(), g.finish_widths([1, 1]), g.gains(), g.finish(2)
+    launches = [i for i, name in enumerate(calls) if name.startswith("eagle_")]
+    assert len({calls[i] for i in launches}) == 21
+    for i in launches:
+        assert calls[i - 1] == "+cpu" and calls[i + 1] == "-cpu", calls[i]
