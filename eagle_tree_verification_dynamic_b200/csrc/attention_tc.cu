@@ -418,10 +418,11 @@ __device__ __forceinline__ int table_entry(const int32_t* bt, int idx, int width
 // (kModeSinks only reports pages that hold a key some row sees: a page between
 // the sinks and the window may have been given back.)
 // Returns false when a wait gave up.
-template <int D, int MODE, typename Lay = TcLayout<D>>
+template <int D, int MODE>
 __device__ bool produce_paged(const TcParams& p, const AttnGeom& a, const Piece& pc, int g, uint32_t s_base,
                               TcBars* bars, volatile int* abort, const CUtensorMap* tm_k, const CUtensorMap* tm_v,
                               const CUtensorMap* tm_kt, const CUtensorMap* tm_vt, int lane, int& jg) {
+  using Lay = TcLayout<D, kWideTiles<MODE>>;
   constexpr int S = Lay::kStages;
   const int ps = p.page_size;
   const int sub = ps < kBN ? ps : kBN;  // keys per box
