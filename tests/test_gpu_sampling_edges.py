@@ -12,7 +12,7 @@ import torch
 import eagle_tree_verification_dynamic_b200 as et
 from oracle import sampling as S
 
-from test_gpu_sampling import DT, check_rows, f32, run_walk, sampling_of, walk_case
+from test_gpu_sampling import DT, check_rows, f32, params_of, run_walk, sampling_of, walk_case
 
 pytestmark = pytest.mark.gpu
 INF = math.inf
@@ -196,3 +196,50 @@ def test_the_argmax_of_a_row_of_values_near_zero(dtype):
     prm = (np.full(B, 10.0, np.float32), np.zeros(B, np.int32), np.ones(B, np.float32), np.zeros(B, np.float32))
     got = run_walk(c, sampling_of(*prm), True)
     assert walks_that_differ(c, prm, True, got) == (0, 0) and got[2].tolist() == [0, 777, V - 1]
+
+
+# ------------------------------------------------------------------ many rows, wide ones, values beyond the bins
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("rows,V", [(300, 9000), (160, 2051), (700, 2048)])
+def test_wide_rows_of_one_cta_each(rows, V, dtype):
+    """The draw over bf16 rows counts a row's parts again before it reads one: rows of one CTA and 256 vectors at least."""
+    rng = np.random.default_rng(V)
+    host = torch.from_numpy((rng.standard_normal((rows, V)) * 3).astype(np.float32)).to(DT[dtype])
+    host[::7] = torch.round(host[::7])                   # many ties at any cut
+    u = rng.random(rows, dtype=np.float32)
+    prm = params_of(rng, rows, V)
+    check_rows(host.double().numpy(), u, *prm, et.sample(host.cuda(), f32(u), sampling_of(*prm)))
+    top = np.full(rows, 0.9, np.float32)
+    check_rows(host.double().numpy(), u, None, None, top, None, et.sample(host.cuda(), f32(u), sampling_of(p=top)))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("rows,V", [(3, 9001), (160, 1500)])
+def test_values_that_no_bin_holds(rows, V, dtype):
+    """Logits of 512 and more in magnitude, NaN of either sign, more tokens around a cut than the list holds."""
+    rng = np.random.default_rng(V)
+    x = rng.standard_normal((rows, V)) * 3
+    x[0::4] *= 200.0                                      # both ends
+    x[1::4] = -600.0 - np.abs(x[1::4])                    # all below
+    x[2::4, V // 3] = 700.0
+    flip = rng.random((rows, V)) < 0.01
+    x[flip & (np.arange(rows) % 4 == 3)[:, None]] = math.nan
+    host = torch.from_numpy(x.astype(np.float32)).to(DT[dtype])
+    host[3::8] = -host[3::8]                              # NaN of the other sign
+    u = rng.random(rows, dtype=np.float32)
+    for t, k, p, m in ((1.0, 0, 0.9, 0.0), (50.0, 0, 0.9, 0.0), (100.0, V // 2, 0.7, 0.001), (3.0, V - 3, 1.0, 0.0)):
+        full = lambda v: np.full(rows, v, np.float32)
+        check_rows(host.double().numpy(), u, full(t), [k] * rows, full(p), full(m),
+                   et.sample(host.cuda(), f32(u), sampling_of(full(t), [k] * rows, full(p), full(m))))
+
+
+@pytest.mark.parametrize("wo", [False, True])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("B,V,n,depth,k", [(7, 50, 10, 3, 4), (20, 1001, 24, 5, 6), (3, 20003, 40, 6, 8),
+                                           (2, 66000, 12, 4, 4), (200, 900, 12, 3, 4), (150, 2600, 6, 2, 3)])
+def test_no_walk_differs(B, V, n, depth, k, dtype, wo):
+    """Those with a decision on a border counted too: 1e-8 of a border is 10 times the weights' error."""
+    c = walk_case(11, B, V, n, depth, k, dtype)
+    prm = params_of(np.random.default_rng(60), B, V)
+    differ, near = walks_that_differ(c, prm, wo, run_walk(c, sampling_of(*prm), wo))
+    assert differ == 0 and near <= 1 + B // 50
