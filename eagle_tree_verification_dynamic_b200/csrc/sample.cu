@@ -1150,11 +1150,13 @@ __device__ __forceinline__ void draw_kept(Team& tm, RowSlice<T> sl, RowStat s, d
                   }, [&](int id, float y) { hit(id, own(s, y)); });
 }
 
-// Four CTAs per SM (64 registers): the passes wait on memory and shared atomics in
-// turn, so more rows in flight count for more than registers (1056 rows of 128256,
-// p = 0.9: 258 us against 293 at three).
+// bf16: four CTAs per SM (64 registers): the passes wait on memory and shared
+// atomics in turn, so more rows in flight count for more than registers (1056 rows
+// of 128256, p = 0.9: 258 us against 293 at three).  fp32: three, as many as shared
+// memory holds (58 KB each with the places inside the bins); 64 registers would
+// spill for nothing.
 template <typename T>
-__global__ void __launch_bounds__(kSmpThreads, 4)
+__global__ void __launch_bounds__(kSmpThreads, sizeof(T) == 2 ? 4 : 3)
 sample_kernel(const T* __restrict__ logits, int V, long long stride, eagle_sampling_t params,
               const float* __restrict__ uniforms, int32_t* __restrict__ tokens, float* __restrict__ logprob, int per) {
   __shared__ SmpShared sm;
