@@ -161,15 +161,17 @@ __device__ __forceinline__ bool kept(const RowStat& s, float x, int id) {
 // and an exponent, 2^(r/32) = exp(r ln2/32) from its series up to r^3 (the next
 // term is below 6e-10 relative), all in fp64: an fp32 weight (error 2^-24) would
 // move the cumulative sums of a wide row by more than a small weight's width and
-// with it the token.
+// with it the token.  Every product that is added to something is an explicit fma:
+// the passes over a row have to find the same sums, so a weight must not depend on
+// what the compiler makes of each copy of this code.
 __device__ __forceinline__ u64 weight(const RowStat& s, const double* tab, float x) {
   if (!((s.top - x) * s.c < 45.5f)) return 0ull;  // also NaN and -inf
   constexpr double kMagic = 6755399441055744.0;   // 1.5 * 2^52: adding it rounds to an integer in the low bits
   constexpr double k1 = kLn2 / 32, k2 = k1 * k1 / 2, k3 = k1 * k1 * k1 / 6;
-  const double t = ((double)s.top - (double)x) * s.c32;
-  const double nm = t + kMagic;
+  const double d = (double)s.top - (double)x;
+  const double nm = fma(d, s.c32, kMagic);
   const int n = __double2loint(nm);
-  const double r = (nm - kMagic) - t;
+  const double r = fma(-d, s.c32, nm - kMagic);
   const double p = r * fma(r, fma(r, k3, k2), k1);
   const double b = tab[n & 31];
   const double e = __hiloint2double(__double2hiint(b) - ((n >> 5) << 20), __double2loint(b));
@@ -1284,7 +1286,7 @@ accept_sampling_kernel(const T* __restrict__ tgt, const T* __restrict__ dft, con
       if (!kept(s, x, id)) return 0.0;
       const u64 w = weight(s, sm.tab, x);
       if (w == 0) return 0.0;
-      return fmax(0.0, (double)w * inv_S - t * exp((double)(float)drow[id] - lse));
+      return fmax(0.0, fma(-t, exp((double)(float)drow[id] - lse), __dmul_rn((double)w, inv_S)));  // (see weight)
     };
     if (len < depth && s.total) {
       int c = 1;
