@@ -28,7 +28,10 @@
 //               window / tree bitmask, keeps its own running reference max
 //               (re-based only when it grows by > 8 in log2 units, then its O
 //               and row sum are rescaled in TMEM) and writes P = 2^(x - m) as
-//               bf16 over the S it has read.  At the end of a unit's piece the
+//               bf16 over the S it has read (the type of V: one product takes
+//               one type; a rounding of up to 2^-8 per weight, which averages
+//               out over the keys, beside the output's own; the row sum adds
+//               the fp32 values).  At the end of a unit's piece the
 //               pair exchanges (max, sum) through shared memory, merges O_A and
 //               O_B, and writes the output or partial
 // Over a shared prefix (wide units, 352 threads) a unit has 256 rows, the two
@@ -142,8 +145,8 @@ enum AttnMode { kModePlain = 0, kModeSinks = 1, kModeShared = 2 };
 // Wide units (256 rows) over a shared prefix: there a CTA streams a hundred tiles
 // and more, and with 128 rows each the loads alone took 1040 of 1190 us (16
 // sequences over 32763 keys, 80-node trees; 5.5 GB, in part past L2).  256 rows:
-// 850 us; 32 sequences over 4096 keys 197 -> 150, 4 over 2048 with a KV head per
-// query head 48 -> 37, 16 over 2048 with 80-node trees 133 -> 114.  A batch of few
+// 850-1000 us; 32 sequences over 4096 keys 197 -> 153, 4 over 2048 with a KV head per
+// query head 48 -> 38, 16 over 2048 with 80-node trees 133 -> 114.  A batch of few
 // rows a head leaves half a unit empty and loses a little: 1 of 128 rows over
 // 32768 keys 75 -> 79, 8 of 32 rows over 8192 keys 35 -> 41.  With sinks every unit
 // has one sequence's rows only: narrow.

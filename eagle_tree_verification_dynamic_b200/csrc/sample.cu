@@ -35,10 +35,12 @@
 // waves of 592.  Per wave and p = 0.9 the counting pass takes 27 us (one shared
 // atomic per logit; HBM alone would need 21), the second count of the CTA the
 // draw falls into (narrow) 36, the cuts 14, the weights 12 and the draw 6:
-// 250 us in all, instruction issue rather than memory.  One to 32 rows: a chain of
-// cluster exchanges of about 1.5 us each, 31-39 us.  An unfiltered row of
-// small positive and negative logits has no short list of values: its draw is
-// bound by the fp64 weights of its own slice (1056 rows: 390 us).
+// 255 us in all, instruction issue rather than memory.  One fp32 row of 32000
+// (top-p): eleven cluster exchanges of about 1.5 us, half of its 33 us; 32 rows 35.
+// An unfiltered row of small positive and negative logits has no short list of
+// values: its draw is bound by the fp64 weights of its own slice (1056 rows: 400 us).
+// Rows cut by halving take 2 to 6 times as long where there are 1 to 32, 5 to 18
+// times where there are hundreds (1056 rows with a logit of 600, top-p: 5 ms).
 #include <cooperative_groups.h>
 
 #include <map>
@@ -1392,9 +1394,13 @@ RowPlan plan_row(long long rows, int V, int elem_bytes) {
   int cl = 1;
   // Few rows: more CTAs each, as long as all fit at two per SM.  A wider cluster
   // shortens the passes and pays for every exchange.  Measured over filters of
-  // all kinds, V = 128256: 1 row, 16 CTAs 17-31 us, one 70-95; 32 rows, 8 or 9
-  // CTAs 30-40 us, one 50-120, 16 (two waves) 50-80; 211 rows, one CTA 60-130 us,
-  // two 85-165; 1056 rows, one 174-390, two 205-350.
+  // all kinds, V = 128256, fp32 / bf16 (us): 1 row, 16 CTAs 26-42 / 23-34, eight
+  // 38-57 / 26-34, one 106-241 / 48-114; 32 rows, nine CTAs 40-77 / 27-38, 16 (two
+  // waves) 51-105 / 44-68, four 52-104 / 33-53; 1056 rows, one 568-938 / 175-404, two
+  // 636-1148 / 207-376.  Between, two CTAs would gain on rows this wide (211 rows,
+  // one 192-344 / 59-155, two 165-310 / 54-116) and lose on narrower ones (32003
+  // tokens: one 56-124 / 36-58, two 79-159 / 36-49; 300 rows of them: one 64-131 /
+  // 42-67, two 116-204 / 58-80).
   const long long want = 2LL * device_sm_count() / rows;
   if (cl < want) cl = (int)(want < kSmpMaxCluster ? want : kSmpMaxCluster);
   if (cl > (all + kSmpThreads - 1) / kSmpThreads) cl = (all + kSmpThreads - 1) / kSmpThreads;  // a vector per thread at least
