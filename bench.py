@@ -311,14 +311,13 @@ def attn_source_digest() -> str:
 ATTN_TRAFFIC_BYTES = {
     # ncu --metrics dram__bytes_read.sum,dram__bytes_write.sum,gpu__time_duration.sum -k regex:attn_tc_kernel
     #     -s 8 -c 1 on `bench.py --config <name> --steps 3 --warmup 3 --no-cpu-baseline --no-per-config`
-    ("7b", 0, "f5510cc048b9f0a0"): 35111936 + 0,
-    ("l3-8b", 0, "f5510cc048b9f0a0"): 204041984 + 5385472,
-    ("serve", 0, "f5510cc048b9f0a0"): 309454080 + 13574400,
-    ("long", 0, "f5510cc048b9f0a0"): 194805504 + 3845632,
-    # the serving mix over a paged cache (`--paged 64` / `--paged 16` added to the command above);
-    # ncu printed these two in MB with two decimals, so they are rounded to 10 kB
-    ("serve", 64, "f5510cc048b9f0a0"): 309370000 + 13850000,
-    ("serve", 16, "f5510cc048b9f0a0"): 309470000 + 13980000,
+    ("7b", 0, "b7879f2c0e5bb0a5"): 35112960 + 0,
+    ("l3-8b", 0, "b7879f2c0e5bb0a5"): 203780096 + 5551872,
+    ("serve", 0, "b7879f2c0e5bb0a5"): 309438976 + 13923840,
+    ("long", 0, "b7879f2c0e5bb0a5"): 194106368 + 5971968,
+    # the serving mix over a paged cache (`--paged 64` / `--paged 16` added to the command above)
+    ("serve", 64, "b7879f2c0e5bb0a5"): 309356800 + 13868288,
+    ("serve", 16, "b7879f2c0e5bb0a5"): 309543680 + 14063616,
 }
 
 
