@@ -498,7 +498,7 @@ __device__ __forceinline__ RowAsk row_ask(const RowParams& pr, int V, RowStat& s
   q.k = greedy || (q.by_p && !(pr.top_p > 0.f)) ? 1 : (pr.top_k > 0 && pr.top_k < V ? pr.top_k : 0);
   if (q.k == 1) q.by_p = false;  // one token is its own share
   q.floor = -INFINITY;
-  if (!greedy && pr.min_p > 0.f) {
+  if (!greedy && pr.min_p > 0.f && T_ < INFINITY) {  // (T infinite: every e is 1)
     // e >= min_p where x >= M + T ln(min_p): the smallest float at or above it
     const double at = pr.min_p >= 1.f ? (double)s.top : (double)s.top + T_ * log((double)pr.min_p);
     q.floor = __double2float_ru(at);

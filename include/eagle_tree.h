@@ -350,7 +350,8 @@ EAGLE_API eagle_status eagle_accept(const void* target_logits, int target_dtype,
 /* -------------------------------------------- sampling under parameters
  * What a request asks of its samples.  DEVICE arrays, one entry per row (for
  * the walk: per sequence); a NULL array leaves that parameter off for all.
- *   temperature  T > 0 (NULL: 1; below 2^-100 as 2^-100); T <= 0 or NaN: greedy,
+ *   temperature  T > 0 (NULL: 1; below 2^-100 as 2^-100; infinite: all tokens
+ *                equally likely); T <= 0 or NaN: greedy,
  *                the argmax alone
  *   top_k        the k likeliest tokens (ties to the lower id); <= 0 or >= V: off
  *   top_p        of those, the fewest likeliest ones whose probability among

@@ -243,3 +243,24 @@ def test_no_walk_differs(B, V, n, depth, k, dtype, wo):
     prm = params_of(np.random.default_rng(60), B, V)
     differ, near = walks_that_differ(c, prm, wo, run_walk(c, sampling_of(*prm), wo))
     assert differ == 0 and near <= 1 + B // 50
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_an_infinite_temperature_makes_all_tokens_equally_likely(dtype):
+    """min-p of 1 and below then removes nothing; top-k and top-p still go by the logits' order."""
+    rng = np.random.default_rng(1)
+    V, rows = 4000, 5
+    host = torch.from_numpy((rng.standard_normal((rows, V)) * 3).astype(np.float32)).to(DT[dtype])
+    host[:, ::2] = -INF
+    alive = np.arange(1, V, 2)
+    u = np.array([0.0, 0.1001, 0.5001, 0.9001, 1.0 - 2.0 ** -24], np.float32)
+    full = lambda v: np.full(rows, v, np.float32)
+    for m in (0.3, 1.0, 2.0):
+        tok, lp = et.sample(host.cuda(), f32(u), sampling_of(full(INF), None, None, full(m)))
+        assert tok.tolist() == [int(alive[int(float(v) * len(alive))]) for v in u]
+        assert (lp.double().cpu() + math.log(len(alive))).abs().max().item() < 1e-6
+    k = 6
+    tok, lp = et.sample(host.cuda(), f32(u), sampling_of(full(INF), [k] * rows, None, full(1.0)))
+    for r in range(rows):
+        ids = sorted(np.argsort(-host[r].double().numpy(), kind="stable")[:k])
+        assert int(tok[r]) == ids[int(float(u[r]) * k)] and abs(float(lp[r]) + math.log(k)) < 1e-6
